@@ -71,8 +71,8 @@ typedef enum { TSENOR_F32 = 0, TSENOR_BF16 = 1 } tsenor_dtype;
 
 typedef enum {
     TSENOR_OK = 0,
-    TSENOR_ERR_ARG = -1,             /* null pointer, bad dtype, N/tau/iters/sweeps out of range (tau: see TSENOR_MAX_TAU), misaligned pointer */
-    TSENOR_ERR_SHAPE = -2,           /* rows or cols negative or not a multiple of M */
+    TSENOR_ERR_ARG = -1,             /* null pointer, bad dtype, N/tau/iters/sweeps out of range (tau: see TSENOR_MAX_TAU), misaligned pointer or leading dimension */
+    TSENOR_ERR_SHAPE = -2,           /* rows or cols negative or not a multiple of M; a size above its call's limit */
     TSENOR_ERR_UNSUPPORTED_M = -3,   /* M not in {4, 8, 16, 32, 64} */
     TSENOR_ERR_CUDA = -4,            /* a CUDA runtime call failed; see tsenor_last_error() */
     TSENOR_ERR_DEVICE = -5,          /* tsenor_error_count: blocks failed on the device (count in *count_out) */
@@ -125,7 +125,8 @@ tsenor_status tsenor_objective(const void* W, tsenor_dtype dtype, int64_t rows, 
 /*
  * Synchronises `stream`, then returns in *count_out the number of blocks that
  * failed on this device (non-finite input, or a rounding step that found no
- * move) since the previous call, and resets the counter.  Returns TSENOR_OK
+ * move) since the previous call, and of rows that failed in the distillation
+ * calls, and resets the counter.  Returns TSENOR_OK
  * when that number is 0 and TSENOR_ERR_DEVICE when it is not (the count is
  * written in both cases); TSENOR_ERR_ARG for a null count_out, TSENOR_ERR_CUDA
  * when the copy or the synchronisation fails.
@@ -252,6 +253,146 @@ tsenor_status tsenor_mask_scores(const float* scores, int64_t rows, int64_t cols
  */
 tsenor_status tsenor_mask_host(const void* W_host, tsenor_dtype dtype, int64_t rows, int64_t cols, int N, int M,
                                float tau, int iters, int sweeps, uint32_t* mask_host, tsenor_stream_t stream);
+
+/*
+ * ---- The pruned layer in 8 bits ------------------------------------------
+ *
+ * Quantisers and products of the masked weights, and the distillation loss
+ * that recovers a pruned model.  The TSENOR review stops at the mask ("Core
+ * claim"); these calls run what the mask is for, the forward product and the
+ * transposed one of the backward pass, from one 8-bit copy of the masked
+ * weights: a scale per 128 x 128 block is transposable as the mask is.
+ *
+ * A quantised matrix of rows x cols is
+ *   values    e4m3 codes (4 exponent bits, 3 fraction bits, bias 7, largest
+ *             448, 0x7f and 0xff NaN), row-major, ld bytes from row to row,
+ *             ld a multiple of 16; 16-byte aligned.
+ *   scales    one byte b, worth 2^(b - 127), per row and block of 128
+ *             columns, for products that sum over the columns.
+ *             tsenor_scale_bytes(rows, cols) bytes, 16-byte aligned: an array
+ *             [ceil(cols/512)][ceil(rows/128)] of 512-byte entries; the byte
+ *             of row r and column c is at (r%32)*16 + (r%128)/32*4 +
+ *             (c/128)%4 of the entry [c/512][r/128].  Bytes of an entry that
+ *             lie past the matrix are written as 127.  b = 255 is NaN.
+ *   scales_t  one byte per column and block of 128 rows, for products that sum
+ *             over the rows: the same with rows and columns exchanged
+ *             (tsenor_scale_bytes(cols, rows) bytes).
+ * This is the order in which the tensor cores take their scales, so the
+ * products read it as it is.
+ */
+typedef enum { TSENOR_BLOCK_ROW = 0, TSENOR_BLOCK_COLUMN = 1, TSENOR_BLOCK_TILE = 2 } tsenor_block;
+typedef enum { TSENOR_NT = 0, TSENOR_NN = 1, TSENOR_TN = 2 } tsenor_form;
+
+/* Bytes of a `scales` array of a rows x cols matrix (0 for an empty one). */
+int64_t tsenor_scale_bytes(int64_t rows, int64_t cols);
+
+/*
+ * e4m3 codes of x with one scale per block: 1 x 128 entries of a row
+ * (TSENOR_BLOCK_ROW, writes scales), 128 x 1 of a column (TSENOR_BLOCK_COLUMN,
+ * writes scales_t) or 128 x 128 (TSENOR_BLOCK_TILE, writes both, each with the
+ * block's byte for all of its rows or columns).  Blocks start at multiples of
+ * 128; the last one may be shorter.
+ * For a block with largest finite magnitude a > 0 the scale is the smallest
+ * power of two, at least 2^-126, with a / scale <= 448; an all-zero block has
+ * scale 1.  The code is x / scale rounded to nearest, ties to even.  NaN and
+ * infinities do not count towards a and get the code 0x7f.
+ *   x:      rows x cols of `dtype`, ldx elements from row to row, aligned to
+ *           its elements; 16-byte aligned rows are read faster.
+ *   mask:   optional rows x ceil(cols/32) words (layout as above): an entry
+ *           whose bit is 0 counts as 0, whatever x holds there.
+ *   values: only columns below `cols` are written.
+ * The arrays that `block` does not write may be NULL.
+ */
+tsenor_status tsenor_quantize(const void* x, tsenor_dtype dtype, int64_t rows, int64_t cols, int64_t ldx,
+                              tsenor_block block, const uint32_t* mask, uint8_t* values, int64_t ldv,
+                              uint8_t* scales, uint8_t* scales_t, tsenor_stream_t stream);
+
+/*
+ * Both TSENOR_BLOCK_ROW (values, scales) and TSENOR_BLOCK_COLUMN (values_t,
+ * scales_t; also rows x cols, not transposed) of one x, which is read once: a
+ * training step sums a batch's activations and gradients over features in one
+ * product and over tokens in another.
+ */
+tsenor_status tsenor_quantize_pair(const void* x, tsenor_dtype dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                   uint8_t* values, int64_t ldv, uint8_t* scales, uint8_t* values_t, int64_t ldv_t,
+                                   uint8_t* scales_t, tsenor_stream_t stream);
+
+/*
+ * What a quantised matrix stands for: code * scale, in `dtype`.
+ *   scales:     `scales` when along_rows is 0, `scales_t` otherwise.
+ *   out:        rows x cols, ldo elements from row to row.
+ */
+tsenor_status tsenor_dequantize(const uint8_t* values, int64_t rows, int64_t cols, int64_t ldv,
+                                const uint8_t* scales, int along_rows, void* out, tsenor_dtype dtype, int64_t ldo,
+                                tsenor_stream_t stream);
+
+/*
+ * Product of two quantised matrices, m x n, summed over k:
+ *   TSENOR_NT  out[i][j] = sum A[i][l] * B[j][l]   A m x k (scales), B n x k (scales)
+ *   TSENOR_NN  out[i][j] = sum A[i][l] * B[l][j]   A m x k (scales), B k x n (scales_t)
+ *   TSENOR_TN  out[i][j] = sum A[l][i] * B[l][j]   A k x m (scales_t), B k x n (scales_t)
+ * With X the tokens of a batch and V a layer's masked weights (TSENOR_BLOCK_TILE):
+ * the forward X V^T is NT, the input gradient dY V is NN, and the weight
+ * gradient dY^T X is TN.  Sums are held in fp32 and rounded once to `dtype`.
+ * The result does not depend on the order in which thread blocks run: the
+ * same call gives the same bits.
+ *   mask:   optional m x ceil(n/32) words: an entry whose bit is 0 is written
+ *           as 0 (a weight gradient of the kept weights only).
+ *   out:    m x n, ldo elements from row to row, aligned to its elements; only
+ *           columns below n are written.  k == 0 writes zeros.
+ */
+tsenor_status tsenor_matmul(tsenor_form form, const uint8_t* a, int64_t lda, const uint8_t* scales_a,
+                            const uint8_t* b, int64_t ldb, const uint8_t* scales_b, int64_t m, int64_t n, int64_t k,
+                            const uint32_t* mask, void* out, tsenor_dtype dtype, int64_t ldo,
+                            tsenor_stream_t stream);
+
+/*
+ * Distillation from a dense teacher's top logits: what a pruned model keeps of
+ * its teacher's outputs, as tsenor_objective says what a mask keeps of the
+ * weights.  Row (token) r has student logits z (vocab of them), teacher entries
+ * (index, top_logits) and temperature T:
+ *   p_j  = exp(top_logits_j / T - c)
+ *   c    = log sum_j exp(top_logits_j / T) when teacher_lse is NULL (p sums to
+ *          1), else teacher_lse[r], the teacher's log-normaliser at temperature
+ *          T over its whole vocabulary (p keeps the teacher's own mass)
+ *   q    = softmax(z / T),  lse = log sum_v exp(z_v / T)
+ *   loss = T^2 sum_j p_j (log p_j - log q_{index_j})
+ *   grad_v = weight * d loss / d z_v
+ *        = weight * T * (q_v sum_j p_j - sum over j with index_j = v of p_j)
+ *   logits:     rows x vocab of `dtype`, ld elements from row to row; -inf is a
+ *               column of probability 0.
+ *   index:      rows x top int32.  A negative index is no entry (rows with
+ *               fewer than `top`).  The same index may occur more than once.
+ *   top_logits: rows x top fp32; -inf is an entry of weight 0.
+ *   weight:     rows fp32, or NULL for 1: the loss's upstream gradient, 0 for
+ *               a token that does not count.
+ * A row without entries (a prompt or padding token) has loss 0 and gradient 0,
+ * whatever its logits hold.  A row that has entries and an index of vocab or
+ * more, a teacher value that is NaN or +inf, a NaN or +inf among its logits, or
+ * no finite logit fails: its loss (and lse) is NaN, its gradient 0, and it is
+ * added to the counter of tsenor_error_count.  The other rows are unaffected.
+ *
+ * tsenor_distill_loss:  loss and lse (for tsenor_distill_grad).
+ * tsenor_distill_step:  loss and gradient from one read of the logits.
+ * tsenor_distill_grad:  the gradient from lse, which the same logits gave.
+ * grad has the type of the logits, ldg elements from row to row; it may be
+ * the logits' own memory (same pointer, ldg == ld).  The sums are fp32 in a
+ * fixed order: the same call gives the same bits.  TSENOR_ERR_SHAPE for top
+ * or vocab above the limits.
+ */
+#define TSENOR_DISTILL_MAX_TOP 1024
+#define TSENOR_DISTILL_MAX_VOCAB 262144
+tsenor_status tsenor_distill_loss(const void* logits, tsenor_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                  const int32_t* index, const float* top_logits, int top, const float* teacher_lse,
+                                  float temperature, float* loss, float* lse, tsenor_stream_t stream);
+tsenor_status tsenor_distill_step(const void* logits, tsenor_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                  const int32_t* index, const float* top_logits, int top, const float* teacher_lse,
+                                  float temperature, const float* weight, float* loss, void* grad, int64_t ldg,
+                                  tsenor_stream_t stream);
+tsenor_status tsenor_distill_grad(const void* logits, tsenor_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                  const int32_t* index, const float* top_logits, int top, const float* teacher_lse,
+                                  float temperature, const float* lse, const float* weight, void* grad, int64_t ldg,
+                                  tsenor_stream_t stream);
 
 /* Static description of a status code. */
 const char* tsenor_status_string(int status);

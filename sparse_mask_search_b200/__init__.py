@@ -6,20 +6,27 @@ no CPU fallback: if the library is missing, importing a function raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
+from typing import NamedTuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libtsenor_b200.so")
 
 TSENOR_F32, TSENOR_BF16 = 0, 1
+BLOCKS = {"row": 0, "column": 1, "tile": 2}
+FORMS = {"nt": 0, "nn": 1, "tn": 2}
 STATUS = {0: "TSENOR_OK", -1: "TSENOR_ERR_ARG", -2: "TSENOR_ERR_SHAPE", -3: "TSENOR_ERR_UNSUPPORTED_M",
           -4: "TSENOR_ERR_CUDA", -5: "TSENOR_ERR_DEVICE", -6: "TSENOR_ERR_TOO_LARGE"}
 NOALLOC_MAX_PARAMS = 16 * 1024 * 1024
+DISTILL_MAX_TOP, DISTILL_MAX_VOCAB = 1024, 262144
 MAX_TAU = 80.0            # TSENOR_MAX_TAU: larger tau is rejected (TSENOR_ERR_ARG)
 EXPORTS = ("tsenor_mask", "tsenor_plan", "tsenor_round", "tsenor_objective", "tsenor_error_count",
            "tsenor_status_string", "tsenor_last_error", "tsenor_mask_noalloc", "tsenor_mask_safeguard",
-           "tsenor_mask_padded", "tsenor_mask_warm", "tsenor_plan_warm", "tsenor_mask_scores", "tsenor_mask_host")
+           "tsenor_mask_padded", "tsenor_mask_warm", "tsenor_plan_warm", "tsenor_mask_scores", "tsenor_mask_host",
+           "tsenor_scale_bytes", "tsenor_quantize", "tsenor_quantize_pair", "tsenor_dequantize", "tsenor_matmul",
+           "tsenor_distill_loss", "tsenor_distill_step", "tsenor_distill_grad")
 
 _lib = None
 
@@ -51,6 +58,15 @@ def lib() -> C.CDLL:
         L.tsenor_round.argtypes = [p, p, i32, i64, i64, i32, i32, i32, p, p]
         L.tsenor_objective.argtypes = [p, i32, i64, i64, p, i32, i32, p, p]
         L.tsenor_error_count.argtypes = [p, C.POINTER(C.c_int64)]
+        L.tsenor_scale_bytes.argtypes = [i64, i64]
+        L.tsenor_scale_bytes.restype = i64
+        L.tsenor_quantize.argtypes = [p, i32, i64, i64, i64, i32, p, p, i64, p, p, p]
+        L.tsenor_quantize_pair.argtypes = [p, i32, i64, i64, i64, p, i64, p, p, i64, p, p]
+        L.tsenor_dequantize.argtypes = [p, i64, i64, i64, p, i32, p, i32, i64, p]
+        L.tsenor_matmul.argtypes = [i32, p, i64, p, p, i64, p, i64, i64, i64, p, p, i32, i64, p]
+        L.tsenor_distill_loss.argtypes = [p, i32, i64, i64, i64, p, p, i32, p, f32, p, p, p]
+        L.tsenor_distill_step.argtypes = [p, i32, i64, i64, i64, p, p, i32, p, f32, p, p, p, i64, p]
+        L.tsenor_distill_grad.argtypes = [p, i32, i64, i64, i64, p, p, i32, p, f32, p, p, p, i64, p]
         L.tsenor_status_string.argtypes = [i32]
         L.tsenor_status_string.restype = C.c_char_p
         L.tsenor_last_error.restype = C.c_char_p
@@ -289,8 +305,324 @@ def tsenor_objective(W, mask, N: int, M: int, out=None, stream=None):
     return out
 
 
+class QuantizedMatrix(NamedTuple):
+    """A matrix in 8 bits: e4m3 codes with one power-of-two scale per block of 128.
+
+    values: torch.float8_e4m3fn (rows, cols), row stride a multiple of 16.
+    scales: uint8 (ceil(cols/512), ceil(rows/128), 512), one byte per row and 128
+    columns, for products that sum over the columns; scales_t: uint8
+    (ceil(rows/512), ceil(cols/128), 512), for products that sum over the rows
+    (the layout stands in include/tsenor.h).  Either may be None.
+    """
+    values: object
+    scales: object = None
+    scales_t: object = None
+
+    @property
+    def shape(self):
+        return tuple(self.values.shape)
+
+
+def scale_shape(rows: int, cols: int) -> tuple[int, int, int]:
+    """Shape of ``scales`` of a rows x cols matrix (of ``scales_t``: with rows and cols exchanged)."""
+    return (cols + 511) // 512, (rows + 127) // 128, 512
+
+
+def _strided(t, name, types):
+    """Row stride of a 2-D CUDA tensor whose rows are dense."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    if t.dtype not in types:
+        raise TypeError(f"{name} must be {' or '.join(str(x) for x in types)}, got {t.dtype}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows")
+    if rows <= 1:
+        return max(cols, t.stride(0))
+    if t.stride(0) < cols:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.stride(0)
+
+
+def _dense(t, name, dtype, shape, device):
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}")
+
+
+def _mask_pointer(mask, rows, cols, device):
+    import torch
+    if mask is None:
+        return None
+    _dense(mask, "mask", torch.int32, (rows, words_per_row(cols)), device)
+    return mask.data_ptr()
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The device and the stream of a call: what it allocates belongs to that stream."""
+    import torch
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+def _launch(fn, device, *args):
+    """fn(*args, stream) on the device's current stream."""
+    import torch
+    _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _needs_guard(device, stream):
+    import torch
+    return stream is not None or torch.cuda.current_device() != device.index
+
+
+def _new_codes(rows, cols, device):
+    import torch
+    ld = (cols + 15) // 16 * 16
+    return torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device)[:, :cols]
+
+
+def _codes(t, name, rows, cols, device):
+    """(pointer, row stride) of a codes tensor."""
+    import torch
+    ld = _strided(t, name, (torch.float8_e4m3fn,))
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    if rows <= 1 or cols == 0:
+        ld = (cols + 15) // 16 * 16
+    if ld % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{name} must have rows that start on 16 bytes (a row stride that is a multiple of 16)")
+    return t.data_ptr(), ld
+
+
+def _new_scales(rows, cols, device):
+    import torch
+    return torch.empty(scale_shape(rows, cols), dtype=torch.uint8, device=device)
+
+
+def _float_types():
+    import torch
+    return torch.bfloat16, torch.float32
+
+
+def tsenor_quantize(X, block: str = "row", mask=None, out=None, stream=None):
+    """X (bfloat16 or float32, dense rows) in 8 bits; returns a QuantizedMatrix.
+
+    block: "row" (a scale per 128 entries of a row: ``scales``), "column" (per 128
+    entries of a column: ``scales_t``) or "tile" (per 128 x 128 entries: both;
+    weights, which both a layer's product and its transposed one read).
+    mask: (rows, ceil(cols/32)) int32 words as tsenor_mask returns them; an entry
+    whose bit is 0 counts as 0.  out: a QuantizedMatrix to write into.
+    """
+    import torch
+    ldx = _strided(X, "X", _float_types())
+    if block not in BLOCKS:
+        raise ValueError(f"block must be one of {', '.join(BLOCKS)}, got {block!r}")
+    if _needs_guard(X.device, stream):
+        with _on(X.device, stream):
+            return tsenor_quantize(X, block, mask, out)
+    rows, cols = X.shape
+    mask_ptr = _mask_pointer(mask, rows, cols, X.device)
+    if out is None:
+        out = QuantizedMatrix(_new_codes(rows, cols, X.device),
+                              _new_scales(rows, cols, X.device) if block != "column" else None,
+                              _new_scales(cols, rows, X.device) if block != "row" else None)
+    else:
+        if block != "column":
+            _dense(out.scales, "out.scales", torch.uint8, scale_shape(rows, cols), X.device)
+        if block != "row":
+            _dense(out.scales_t, "out.scales_t", torch.uint8, scale_shape(cols, rows), X.device)
+    values, ldv = _codes(out.values, "out.values", rows, cols, X.device)
+    _launch(lib().tsenor_quantize, X.device, X.data_ptr(), _dtype_code(X), rows, cols, ldx, BLOCKS[block], mask_ptr,
+            values, ldv, out.scales.data_ptr() if block != "column" else None,
+            out.scales_t.data_ptr() if block != "row" else None)
+    return out
+
+
+def tsenor_quantize_pair(X, stream=None):
+    """(tsenor_quantize(X, "row"), tsenor_quantize(X, "column")) from one read of X."""
+    ldx = _strided(X, "X", _float_types())
+    if _needs_guard(X.device, stream):
+        with _on(X.device, stream):
+            return tsenor_quantize_pair(X)
+    rows, cols = X.shape
+    q = QuantizedMatrix(_new_codes(rows, cols, X.device), _new_scales(rows, cols, X.device), None)
+    t = QuantizedMatrix(_new_codes(rows, cols, X.device), None, _new_scales(cols, rows, X.device))
+    ldv = (cols + 15) // 16 * 16
+    _launch(lib().tsenor_quantize_pair, X.device, X.data_ptr(), _dtype_code(X), rows, cols, ldx, q.values.data_ptr(),
+            ldv, q.scales.data_ptr(), t.values.data_ptr(), ldv, t.scales_t.data_ptr())
+    return q, t
+
+
+def tsenor_dequantize(Q, dtype=None, out=None, stream=None):
+    """What a QuantizedMatrix stands for, in bfloat16 or float32 (default); by ``scales`` where it has them."""
+    import torch
+    device = Q.values.device
+    rows, cols = Q.shape
+    ldv = _strided(Q.values, "Q.values", (torch.float8_e4m3fn,))
+    if Q.scales is not None:
+        _dense(Q.scales, "Q.scales", torch.uint8, scale_shape(rows, cols), device)
+    elif Q.scales_t is not None:
+        _dense(Q.scales_t, "Q.scales_t", torch.uint8, scale_shape(cols, rows), device)
+    else:
+        raise ValueError("Q has no scales")
+    if _needs_guard(device, stream):
+        with _on(device, stream):
+            return tsenor_dequantize(Q, dtype, out)
+    out, ldo = _output(out, rows, cols, dtype or torch.float32, device)
+    scales = Q.scales if Q.scales is not None else Q.scales_t
+    _launch(lib().tsenor_dequantize, device, Q.values.data_ptr(), rows, cols, ldv, scales.data_ptr(),
+            int(Q.scales is None), out.data_ptr(), _dtype_code(out), ldo)
+    return out
+
+
+def _output(out, rows, cols, dtype, device):
+    """(out, row stride): a given output checked, or a new one."""
+    import torch
+    if out is None:
+        if dtype not in _float_types():
+            raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+        return torch.empty((rows, cols), dtype=dtype, device=device), max(cols, 1)
+    ldo = _strided(out, "out", _float_types())
+    if out.device != device:
+        raise ValueError(f"out must be on {device}")
+    if tuple(out.shape) != (rows, cols):
+        raise ValueError(f"out must have shape {(rows, cols)}, got {tuple(out.shape)}")
+    return out, ldo
+
+
+def tsenor_matmul(A, B, form: str = "nt", mask=None, dtype=None, out=None, stream=None):
+    """Product of two QuantizedMatrix operands, summed in fp32.
+
+    form "nt": A (m, k) @ B (n, k).T by A.scales and B.scales;
+    "nn": A (m, k) @ B (k, n) by A.scales and B.scales_t;
+    "tn": A (k, m).T @ B (k, n) by A.scales_t and B.scales_t.
+    mask: optional (m, ceil(n/32)) int32 words; entries whose bit is 0 are written
+    as 0.  dtype: torch.bfloat16 (default) or torch.float32, that of ``out`` when it is given.
+    """
+    import torch
+    if form not in FORMS:
+        raise ValueError(f"form must be one of {', '.join(FORMS)}, got {form!r}")
+    device = A.values.device
+    if not A.values.is_cuda:
+        raise ValueError("A must be on a CUDA device")
+    if _needs_guard(device, stream):
+        with _on(device, stream):
+            return tsenor_matmul(A, B, form, mask, dtype, out)
+    (ra, ca), (rb, cb) = A.shape, B.shape
+    m, k = (ca, ra) if form == "tn" else (ra, ca)
+    n, kb = (rb, cb) if form == "nt" else (cb, rb)
+    if k != kb:
+        raise ValueError(f"the operands sum over {k} and {kb} entries")
+    a, lda = _codes(A.values, "A.values", ra, ca, device)
+    b, ldb = _codes(B.values, "B.values", rb, cb, device)
+    sa, sb = (A.scales_t if form == "tn" else A.scales), (B.scales if form == "nt" else B.scales_t)
+    if sa is None or sb is None:
+        raise ValueError(f'form "{form}" needs {"A.scales_t" if form == "tn" else "A.scales"} and '
+                         f'{"B.scales" if form == "nt" else "B.scales_t"}')
+    _dense(sa, "A's scales", torch.uint8, scale_shape(m, k), device)
+    _dense(sb, "B's scales", torch.uint8, scale_shape(n, k), device)
+    mask_ptr = _mask_pointer(mask, m, n, device)
+    if dtype is not None and out is not None and out.dtype != dtype:
+        raise TypeError(f"out is {out.dtype}, dtype {dtype}")
+    out, ldo = _output(out, m, n, dtype or torch.bfloat16, device)
+    _launch(lib().tsenor_matmul, device, FORMS[form], a, lda, sa.data_ptr(), b, ldb, sb.data_ptr(), m, n, k, mask_ptr,
+            out.data_ptr(), _dtype_code(out), ldo)
+    return out
+
+
+def _distill_args(logits, index, top_logits, temperature, teacher_lse):
+    """The arguments the distillation calls share, checked."""
+    import torch
+    ld = _strided(logits, "logits", _float_types())
+    rows, vocab = logits.shape
+    if index.dim() != 2 or index.shape[0] != rows:
+        raise ValueError(f"index must have shape ({rows}, top), got {tuple(index.shape)}")
+    top = index.shape[1]
+    _dense(index, "index", torch.int32, (rows, top), logits.device)
+    _dense(top_logits, "top_logits", torch.float32, (rows, top), logits.device)
+    if teacher_lse is not None:
+        _dense(teacher_lse, "teacher_lse", torch.float32, (rows,), logits.device)
+    return (logits.data_ptr(), _dtype_code(logits), rows, vocab, ld, index.data_ptr(), top_logits.data_ptr(), top,
+            teacher_lse.data_ptr() if teacher_lse is not None else None, float(temperature))
+
+
+def _distill_grad_args(logits, weight, grad):
+    import torch
+    rows, vocab = logits.shape
+    if weight is not None:
+        _dense(weight, "weight", torch.float32, (rows,), logits.device)
+    if grad is None:
+        grad, ldg = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device), vocab
+    else:
+        ldg = _strided(grad, "grad", (logits.dtype,))
+        if grad.shape != logits.shape or grad.device != logits.device:
+            raise ValueError(f"grad must have shape {tuple(logits.shape)} on {logits.device}")
+    return grad, (weight.data_ptr() if weight is not None else None), ldg
+
+
+def tsenor_distill_loss(logits, index, top_logits, temperature: float = 1.0, teacher_lse=None, stream=None):
+    """Distillation loss of each row from the teacher's top logits; returns (loss, lse), fp32 (rows,).
+
+    logits: (rows, vocab) bfloat16 or float32 of the student.  index: (rows, top)
+    int32, negative where a row has fewer entries; top_logits: (rows, top) float32.
+    loss = T^2 sum_j p_j (log p_j - log softmax(logits / T)[index_j]) with p the
+    softmax of top_logits / T over the row's entries, or, with teacher_lse (rows,)
+    float32, exp(top_logits / T - teacher_lse).  lse is what tsenor_distill_grad takes.
+    """
+    import torch
+    if logits.is_cuda and _needs_guard(logits.device, stream):
+        with _on(logits.device, stream):
+            return tsenor_distill_loss(logits, index, top_logits, temperature, teacher_lse)
+    args = _distill_args(logits, index, top_logits, temperature, teacher_lse)
+    loss = torch.empty((logits.shape[0],), dtype=torch.float32, device=logits.device)
+    lse = torch.empty_like(loss)
+    _launch(lib().tsenor_distill_loss, logits.device, *args, loss.data_ptr(), lse.data_ptr())
+    return loss, lse
+
+
+def tsenor_distill_step(logits, index, top_logits, temperature: float = 1.0, teacher_lse=None, weight=None, grad=None,
+                        stream=None):
+    """Loss of each row and weight * d loss / d logits from one read of the logits; returns (loss, grad).
+
+    weight: (rows,) float32, default 1: the upstream gradient of each row's loss.
+    grad: optional output like the logits, which may be the logits themselves.
+    """
+    import torch
+    if logits.is_cuda and _needs_guard(logits.device, stream):
+        with _on(logits.device, stream):
+            return tsenor_distill_step(logits, index, top_logits, temperature, teacher_lse, weight, grad)
+    args = _distill_args(logits, index, top_logits, temperature, teacher_lse)
+    grad, weight_ptr, ldg = _distill_grad_args(logits, weight, grad)
+    loss = torch.empty((logits.shape[0],), dtype=torch.float32, device=logits.device)
+    _launch(lib().tsenor_distill_step, logits.device, *args, weight_ptr, loss.data_ptr(), grad.data_ptr(), ldg)
+    return loss, grad
+
+
+def tsenor_distill_grad(logits, index, top_logits, lse, temperature: float = 1.0, teacher_lse=None, weight=None,
+                        grad=None, stream=None):
+    """weight * d loss / d logits, by the lse that tsenor_distill_loss gave for these logits; returns grad."""
+    import torch
+    if logits.is_cuda and _needs_guard(logits.device, stream):
+        with _on(logits.device, stream):
+            return tsenor_distill_grad(logits, index, top_logits, lse, temperature, teacher_lse, weight, grad)
+    args = _distill_args(logits, index, top_logits, temperature, teacher_lse)
+    _dense(lse, "lse", torch.float32, (logits.shape[0],), logits.device)
+    grad, weight_ptr, ldg = _distill_grad_args(logits, weight, grad)
+    _launch(lib().tsenor_distill_grad, logits.device, *args, lse.data_ptr(), weight_ptr, grad.data_ptr(), ldg)
+    return grad
+
+
 def tsenor_error_count(stream=None) -> int:
-    """Blocks that failed since the previous call (synchronises the stream).
+    """Blocks (and rows of the distillation calls) that failed since the previous call (synchronises the stream).
 
     The C call reports a nonzero count with TSENOR_ERR_DEVICE; here the count
     itself is the result, so that status is not raised.
@@ -304,4 +636,6 @@ def tsenor_error_count(stream=None) -> int:
 
 __all__ = ["tsenor_mask", "tsenor_mask_host", "tsenor_mask_scores", "tsenor_mask_noalloc", "tsenor_mask_safeguard", "tsenor_mask_padded", "tsenor_mask_warm",
            "tsenor_plan", "tsenor_plan_warm", "tsenor_round", "tsenor_objective", "tsenor_error_count",
+           "QuantizedMatrix", "scale_shape", "tsenor_quantize", "tsenor_quantize_pair", "tsenor_dequantize",
+           "tsenor_matmul", "tsenor_distill_loss", "tsenor_distill_step", "tsenor_distill_grad",
            "TsenorError", "lib", "words_per_row", "EXPORTS", "LIB_PATH"]

@@ -8,8 +8,8 @@
 
 #include <cudaTypedefs.h>
 
-#include "../../include/tsenor.h"
 #include "common.cuh"
+#include "host.h"
 #include "dykstra.cuh"
 #include "round_warp.cuh"
 #include "round_group.cuh"
@@ -21,12 +21,14 @@ namespace {
 
 thread_local char g_last_error[256] = "";
 
+}  // namespace
+
 tsenor_status cuda_fail(cudaError_t e, const char* what) {
     std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s", what, cudaGetErrorString(e));
     return TSENOR_ERR_CUDA;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+namespace {
 
 tsenor_status check_common(const void* W, int dtype, int64_t rows, int64_t cols, int N, int M) {
     if (M != 4 && M != 8 && M != 16 && M != 32 && M != 64) return TSENOR_ERR_UNSUPPORTED_M;
@@ -597,7 +599,7 @@ extern "C" tsenor_status tsenor_error_count(tsenor_stream_t stream, int64_t* cou
     const unsigned long long zero = 0;
     cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_block_failures, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_block_failures, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess) e = read_row_failures(st, &v);          // synchronises st
     if (e != cudaSuccess) return cuda_fail(e, "tsenor_error_count");
     *count_out = int64_t(v);
     return v ? TSENOR_ERR_DEVICE : TSENOR_OK;
@@ -607,10 +609,10 @@ extern "C" const char* tsenor_status_string(int status) {
     switch (status) {
         case TSENOR_OK: return "ok";
         case TSENOR_ERR_ARG: return "invalid argument";
-        case TSENOR_ERR_SHAPE: return "rows/cols not a non-negative multiple of M";
+        case TSENOR_ERR_SHAPE: return "rows/cols not a non-negative multiple of M, or a size above its limit";
         case TSENOR_ERR_UNSUPPORTED_M: return "M must be 4, 8, 16, 32 or 64";
         case TSENOR_ERR_CUDA: return "CUDA runtime error";
-        case TSENOR_ERR_DEVICE: return "blocks failed on the device (non-finite input or no repair move); see the count";
+        case TSENOR_ERR_DEVICE: return "blocks or rows failed on the device (non-finite input, no repair move, bad index); see the count";
         case TSENOR_ERR_TOO_LARGE: return "rows*cols exceeds TSENOR_NOALLOC_MAX_PARAMS (16777216) of tsenor_mask_noalloc";
         default: return "unknown status";
     }
