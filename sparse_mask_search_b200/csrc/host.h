@@ -18,5 +18,7 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 // Adds the rows that failed in the distillation kernels on the current device
 // since the last call to *count and resets them (ordered on `st`).
 cudaError_t read_row_failures(cudaStream_t st, unsigned long long* count);
+// The same for the threads of tsenor_matmul's kernels whose bounded wait ran out.
+cudaError_t read_stalled(cudaStream_t st, unsigned long long* count);
 
 }  // namespace tsenor

@@ -1,80 +1,290 @@
 // Product of two e4m3 matrices with a power-of-two scale per block of 128 along
 // the contracted axis:
 //   nt  out[m,n] = sum_k A[m,k] B[n,k]     nn  A[m,k] B[k,n]     tn  A[k,m] B[k,n]
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "host.h"
+#include "tensor.h"
 
 namespace tsenor {
 namespace {
 
 struct MatmulArgs {
-    const uint8_t *a, *b;
-    int64_t lda, ldb;
     const uint8_t *sa, *sb;
     int64_t m, n, k;
     const uint32_t* mask;
     int64_t wpr;
     void* out;
     int64_t ldo;
-    bool a_t, b_t;          // the operand is stored with its contracted axis along rows
+    int64_t tiles_m, tiles_n;   // of 128
+    int a_bytes;                // bytes that one TMA copy of an A tile writes
+    int stages;
+    bool a_t, b_t;              // the operand is stored with its contracted axis along rows
     bool bf16;
+    bool vec;                   // four outputs of a row can be stored at once
 };
 
-__device__ __forceinline__ float decode(uint32_t u) {
-    const uint32_t e = (u >> 3) & 15u, f = u & 7u;
-    float x = e ? __uint_as_float(((e + 120u) << 23) | (f << 20)) : float(f) * 0.001953125f;
-    if ((u & 127u) == 127u) x = NAN;
-    return u & 128u ? -x : x;
-}
-__device__ __forceinline__ float power(uint32_t b) {
-    return b == 255u ? NAN : b ? __uint_as_float(b << 23) : __uint_as_float(0x400000u);
-}
-__device__ __forceinline__ float operand(const uint8_t* v, int64_t ld, const uint8_t* s, bool t, int64_t i, int64_t n,
-                                         int64_t k) {
-    const uint32_t b = s[((k / 512) * ((n + 127) / 128) + i / 128) * 512 + (i % 32) * 16 + (i % 128) / 32 * 4 + (k / 128) % 4];
-    return decode(t ? v[k * ld + i] : v[i * ld + k]) * power(b);
+__device__ unsigned long long g_stalled;
+
+constexpr int kTile = 128;                       // rows, columns and summed entries of a tile
+constexpr int kTileBytes = kTile * kTile;
+constexpr int kScaleBytes = 512;
+constexpr int kThreads = 128;
+constexpr int kTmemCols = 256;                   // 128 of the accumulator, 4 of each side's scales
+constexpr int kPad = 132;                        // floats to a staged row: 16-byte stores without bank conflicts
+
+// Shared memory of split_kernel from its 1024-byte aligned base: the A tiles (which may be shorter than 128
+// rows: the rows behind them are read by the tensor core and go to rows of the
+// accumulator that nothing reads), the B tiles, the scales, the barriers.  The
+// fp32 accumulators are staged over the tiles at the end.
+struct SplitSmem {
+    unsigned a, b, s, bars;
+    __host__ __device__ SplitSmem(int stages, int a_bytes) {
+        a = 0;
+        b = stages * a_bytes;
+        s = b + stages * kTileBytes;
+        bars = s + stages * 2 * kScaleBytes;
+        const unsigned staged = kTile * kPad * 4;
+        if (bars < staged) bars = staged;
+    }
+    __host__ __device__ unsigned bytes(int stages) const { return bars + (2 * stages + 1) * 8 + 16; }
+};
+
+__device__ __forceinline__ uint16_t to_bf16(float x) {
+    uint16_t h;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(x));
+    return h;
 }
 
-// 64 x 64 outputs per block of 256 threads, 32 of the contracted axis at a time
-// through shared memory in fp32.
-__global__ void __launch_bounds__(256) matmul_kernel(const MatmulArgs p) {
-    __shared__ float as[32][65], bs[32][65];
-    const int t = threadIdx.x;
-    const int64_t tn = (p.n + 63) / 64;
-    const int64_t m0 = blockIdx.x / tn * 64, n0 = blockIdx.x % tn * 64;
-    const int ty = t / 16 * 4, tx = t % 16 * 4;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < p.k; k0 += 32) {
-        for (int e = t; e < 64 * 32; e += 256) {
-            const int ia = p.a_t ? e % 64 : e / 32, ka = p.a_t ? e / 64 : e % 32;
-            const int ib = p.b_t ? e % 64 : e / 32, kb = p.b_t ? e / 64 : e % 32;
-            as[ka][ia] = m0 + ia < p.m && k0 + ka < p.k ? operand(p.a, p.lda, p.sa, p.a_t, m0 + ia, p.m, k0 + ka) : 0.f;
-            bs[kb][ib] = n0 + ib < p.n && k0 + kb < p.k ? operand(p.b, p.ldb, p.sb, p.b_t, n0 + ib, p.n, k0 + kb) : 0.f;
+// Four sums of row r from column c on: mask, rounding, store.
+__device__ __forceinline__ void store4(const MatmulArgs& p, int64_t r, int64_t c, float4 v) {
+    float x[4] = {v.x, v.y, v.z, v.w};
+    if (p.mask) {
+        const uint32_t w = p.mask[r * p.wpr + c / 32] >> (c % 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = (w >> i) & 1u ? x[i] : 0.f;
+    }
+    if (p.bf16) {
+        uint16_t* o = static_cast<uint16_t*>(p.out) + r * p.ldo + c;
+        if (p.vec && c + 4 <= p.n) {
+            *reinterpret_cast<uint2*>(o) = make_uint2(to_bf16(x[0]) | (uint32_t(to_bf16(x[1])) << 16),
+                                                      to_bf16(x[2]) | (uint32_t(to_bf16(x[3])) << 16));
+        } else {
+            for (int i = 0; i < 4; ++i)
+                if (c + i < p.n) o[i] = to_bf16(x[i]);
         }
-        __syncthreads();
-        for (int k = 0; k < 32; ++k)
+    } else {
+        float* o = static_cast<float*>(p.out) + r * p.ldo + c;
+        if (p.vec && c + 4 <= p.n) {
+            *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
+        } else {
+            for (int i = 0; i < 4; ++i)
+                if (c + i < p.n) o[i] = x[i];
+        }
+    }
+}
+
+// One 128 x 128 tile of the output to a cluster of `split` CTAs; each sums its
+// share of the blocks of 128 in its tensor memory, and the shares are added in
+// rank order through distributed shared memory.  Warp 0 loads (TMA, a ring of
+// stages), warp 1 issues the products, all four warps store.
+__global__ void __launch_bounds__(kThreads)
+split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const MatmulArgs p,
+             const int split) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const SplitSmem at(p.stages, p.a_bytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + at.bars);
+    uint64_t* empty = full + p.stages;
+    uint64_t* done = empty + p.stages;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned rank = split > 1 ? cluster_rank() : 0;
+    const int64_t tile = blockIdx.x / split;
+    const int64_t tm = tile % p.tiles_m, tn = tile / p.tiles_m;
+    const int64_t blocks = (p.k + kTile - 1) / kTile;
+    const int64_t k0 = blocks * rank / split, k1 = blocks * (rank + 1) / split;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        mbar_init(done, 1);
+        mbar_init_fence();
+    }
+    if (warp == 2) tmem_alloc<1>(slot, kTmemCols);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = *slot;
+    bool stalled = false;
+
+    if (warp == 0 && lane == 0) {
+        int st = 0;
+        unsigned phase = 0;
+        int64_t issued = 0;
+        for (int64_t kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait_bounded(empty + st, phase ^ 1)) { stalled = true; break; }
+            const bool scales = kb == k0 || kb % 4 == 0;
+            mbar_arrive_expect_tx(full + st, p.a_bytes + kTileBytes + (scales ? 2 * kScaleBytes : 0));
+            const int k = int(kb * kTile), m = int(tm * kTile), n = int(tn * kTile);
+            tma_load_2d(smem + at.a + st * p.a_bytes, &map_a, p.a_t ? m : k, p.a_t ? k : m, full + st);
+            tma_load_2d(smem + at.b + st * kTileBytes, &map_b, p.b_t ? n : k, p.b_t ? k : n, full + st);
+            if (scales) {
+                uint8_t* d = smem + at.s + st * 2 * kScaleBytes;
+                bulk_load(d, p.sa + ((kb / 4) * p.tiles_m + tm) * kScaleBytes, kScaleBytes, full + st);
+                bulk_load(d + kScaleBytes, p.sb + ((kb / 4) * p.tiles_n + tn) * kScaleBytes, kScaleBytes, full + st);
+            }
+            ++issued;
+            if (++st == p.stages) { st = 0; phase ^= 1; }
+        }
+        // copies in flight end before the block does
+        if (stalled)
+            for (int i = 0; i < p.stages && i < issued; ++i)
+                mbar_wait_bounded(full + i, unsigned((issued - 1 - i) / p.stages) & 1);
+    } else if (warp == 1 && lane == 0) {
+        const uint32_t idesc = mma_desc(kTile, kTile, p.a_t, p.b_t);
+        // 32 of the contracted axis: 32 bytes of a row, or 32 rows
+        const uint32_t step_a = (p.a_t ? 4096 : 32) >> 4, step_b = (p.b_t ? 4096 : 32) >> 4;
+        const uint32_t ts = tmem + kTile;
+        int st = 0;
+        unsigned phase = 0;
+        for (int64_t kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait_bounded(full + st, phase)) { stalled = true; break; }
+            tmem_fence_after();
+            if (kb == k0 || kb % 4 == 0) {
+                const uint32_t s = smem_u32(smem + at.s + st * 2 * kScaleBytes);
+                copy_scales<1>(ts, scale_desc(s));
+                copy_scales<1>(ts + 4, scale_desc(s + kScaleBytes));
+            }
+            const uint32_t id = with_scale_byte(idesc, uint32_t(kb % 4));
+            const uint64_t da = tile_desc(smem_u32(smem + at.a + st * p.a_bytes), kTileBytes);
+            const uint64_t db = tile_desc(smem_u32(smem + at.b + st * kTileBytes), kTileBytes);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[k][ty + i], bs[k][tx + j], acc[i][j]);
-        __syncthreads();
+                mma_scaled<1>(tmem, da + i * step_a, db + i * step_b, id, ts, ts + 4, kb > k0 || i > 0);
+            mma_commit(empty + st);
+            if (++st == p.stages) { st = 0; phase ^= 1; }
+        }
+        if (k1 > k0) mma_commit(done);
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = m0 + ty + i, c = n0 + tx + j;
-            if (r >= p.m || c >= p.n) continue;
-            const float x = !p.mask || ((p.mask[r * p.wpr + c / 32] >> (c % 32)) & 1u) ? acc[i][j] : 0.f;
-            if (p.bf16) {
-                uint16_t h;
-                asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(x));
-                static_cast<uint16_t*>(p.out)[r * p.ldo + c] = h;
-            } else {
-                static_cast<float*>(p.out)[r * p.ldo + c] = x;
+    __syncwarp();
+    // the sums of a share may take long: the wait's bound grows with their number
+    bool ready = k1 == k0;
+    for (int64_t i = 0; i <= (k1 - k0) / 64 && !ready; ++i) ready = mbar_wait_bounded(done, 0);
+    if (!ready) stalled = true;
+    tmem_fence_after();
+
+    const int64_t rows = p.m - tm * kTile < kTile ? p.m - tm * kTile : kTile;
+    float* staged = reinterpret_cast<float*>(smem);
+    {
+        const int r = warp * 32 + lane;
+        if (warp * 32 < rows) {
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+                uint32_t v[32];
+                tmem_load32(tmem + (uint32_t(warp * 32) << 16) + c, v);
+                tmem_wait_load();
+                if (r < rows) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4*>(staged + r * kPad + c + i) =
+                            k1 > k0 ? make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_uint4(0, 0, 0, 0);
+                }
             }
         }
+    }
+    if (stalled) atomicAdd(&g_stalled, 1ull);
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 2) tmem_free<1>(tmem, kTmemCols);
+    if (split > 1) cluster_sync();
+    const uint32_t base = smem_u32(staged);
+    for (int u = int(rank) * kThreads + threadIdx.x; u < rows * (kTile / 4); u += split * kThreads) {
+        const int r = u / (kTile / 4), c = u % (kTile / 4) * 4;
+        if (tn * kTile + c >= p.n) continue;
+        float4 v = *reinterpret_cast<const float4*>(staged + r * kPad + c);
+        if (split > 1) {
+            v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int q = 0; q < split; ++q) {
+                const float4 w = cluster_load4(cluster_addr(base + (r * kPad + c) * 4, q));
+                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+            }
+        }
+        store4(p, tm * kTile + r, tn * kTile + c, v);
+    }
+    if (split > 1) cluster_sync();               // a peer's shared memory lives until all have read it
+}
+
+// Tensor map of an operand's codes, tiles of 128 bytes x `box_rows` in the 128-byte swizzle.
+PFN_cuTensorMapEncodeTiled g_encode = nullptr;
+std::once_flag g_encode_flag;
+
+cudaError_t encode_map(CUtensorMap* map, const uint8_t* v, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    std::call_once(g_encode_flag, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled>(fn);
+    });
+    if (!g_encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};      // columns past the matrix read as 0
+    const cuuint64_t strides[1] = {cuuint64_t(ld)};
+    const cuuint32_t box[2] = {kTile, cuuint32_t(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(v), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_split(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, cudaStream_t st) {
+    // rows of an A tile that a copy brings: no more than there are
+    const int box_a = p.a_t || p.m >= kTile ? kTile : int((p.m + 7) / 8 * 8);
+    p.a_bytes = box_a * kTile;
+    CUtensorMap map_a, map_b;
+    cudaError_t e = p.a_t ? encode_map(&map_a, a, p.k, p.m, lda, kTile) : encode_map(&map_a, a, p.m, p.k, lda, box_a);
+    if (e == cudaSuccess) e = p.b_t ? encode_map(&map_b, b, p.k, p.n, ldb, kTile) : encode_map(&map_b, b, p.n, p.k, ldb, kTile);
+    if (e != cudaSuccess) return e;
+    // two CTAs to an SM
+    p.stages = (110 * 1024) / (p.a_bytes + kTileBytes + 2 * kScaleBytes);
+    const int64_t tiles = p.tiles_m * p.tiles_n, blocks = (p.k + kTile - 1) / kTile;
+    int split = 1;
+    while (split < 8 && tiles * split < 148 && blocks / (2 * split) >= 2) split *= 2;
+    const unsigned bytes = SplitSmem(p.stages, p.a_bytes).bytes(p.stages) + 1024;
+    e = cudaFuncSetAttribute(split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(tiles * split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, split_kernel, map_a, map_b, p, split);
 }
 
 }  // namespace
+
+cudaError_t read_stalled(cudaStream_t st, unsigned long long* count) {
+    unsigned long long v = 0;
+    const unsigned long long zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_stalled, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_stalled, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess) *count += v;
+    return e;
+}
+
 }  // namespace tsenor
 
 using namespace tsenor;
@@ -87,7 +297,7 @@ extern "C" tsenor_status tsenor_matmul(tsenor_form form, const uint8_t* a, int64
     if (dtype != TSENOR_F32 && dtype != TSENOR_BF16) return TSENOR_ERR_ARG;
     const int64_t most = (int64_t(1) << 31) - 1;
     if (m < 0 || n < 0 || k < 0 || m > most || n > most || k > most) return TSENOR_ERR_SHAPE;
-    if (((m + 63) / 64) * ((n + 63) / 64) > most) return TSENOR_ERR_SHAPE;
+    if (((m + kTile - 1) / kTile) * ((n + kTile - 1) / kTile) > most / 8) return TSENOR_ERR_SHAPE;
     if (m == 0 || n == 0) return TSENOR_OK;
     const size_t es = dtype == TSENOR_BF16 ? 2 : 4;
     if (!out || !aligned(out, es) || ldo < n || !aligned(mask, 4)) return TSENOR_ERR_ARG;
@@ -100,9 +310,22 @@ extern "C" tsenor_status tsenor_matmul(tsenor_form form, const uint8_t* a, int64
     if (!a || !aligned(a, 16) || lda % 16 || lda < (a_t ? m : k) || !b || !aligned(b, 16) || ldb % 16 ||
         ldb < (b_t ? n : k) || !scales_a || !aligned(scales_a, 16) || !scales_b || !aligned(scales_b, 16))
         return TSENOR_ERR_ARG;
-    const MatmulArgs p{a, b, lda, ldb, scales_a, scales_b, m, n, k, mask, (n + 31) / 32, out, ldo, a_t, b_t,
-                       dtype == TSENOR_BF16};
-    matmul_kernel<<<unsigned(((m + 63) / 64) * ((n + 63) / 64)), 256, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    MatmulArgs p{};
+    p.sa = scales_a;
+    p.sb = scales_b;
+    p.m = m;
+    p.n = n;
+    p.k = k;
+    p.mask = mask;
+    p.wpr = (n + 31) / 32;
+    p.out = out;
+    p.ldo = ldo;
+    p.tiles_m = (m + kTile - 1) / kTile;
+    p.tiles_n = (n + kTile - 1) / kTile;
+    p.a_t = a_t;
+    p.b_t = b_t;
+    p.bf16 = dtype == TSENOR_BF16;
+    p.vec = aligned(out, 4 * es) && ldo % 4 == 0;
+    const cudaError_t e = launch_split(p, a, lda, b, ldb, st);
     return e == cudaSuccess ? TSENOR_OK : cuda_fail(e, "tsenor_matmul launch");
 }

@@ -600,6 +600,7 @@ extern "C" tsenor_status tsenor_error_count(tsenor_stream_t stream, int64_t* cou
     cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_block_failures, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_block_failures, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
     if (e == cudaSuccess) e = read_row_failures(st, &v);          // synchronises st
+    if (e == cudaSuccess) e = read_stalled(st, &v);
     if (e != cudaSuccess) return cuda_fail(e, "tsenor_error_count");
     *count_out = int64_t(v);
     return v ? TSENOR_ERR_DEVICE : TSENOR_OK;
