@@ -220,11 +220,241 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     if (split > 1) cluster_sync();               // a peer's shared memory lives until all have read it
 }
 
-// Tensor map of an operand's codes, tiles of 128 bytes x `box_rows` in the 128-byte swizzle.
+// ---- large products -------------------------------------------------------------------
+//
+// A pair of CTAs works on a 256 x 256 tile (cta_group::2): each holds 128 rows of
+// A and 128 of B in shared memory and 128 rows of the accumulator.  The pairs are
+// persistent.  Two accumulators of 256 columns and the scales do not fit into
+// 512 columns of tensor memory, so the second one starts at column 240: its
+// product may start once the 32 columns that hold the overlap have been read, which
+// the epilogue does first.
+constexpr int kPairThreads = 256;                // warps: 0 loads, 1 products, 2 tensor memory, 4-7 epilogue
+constexpr int kPairTile = 256;
+constexpr int kPairStages = 6;
+constexpr int kSecond = 240, kScaleA = 496, kScaleB = 500;
+constexpr int kGroupM = 16;                      // tiles of 256 rows walked together, so that B is read from L2
+
+struct PairSmem {
+    static constexpr unsigned a = 0, b = kPairStages * kTileBytes, s = 2 * b, staged = s + kPairStages * 3 * kScaleBytes,
+                              bars = staged + 4 * 32 * 33 * 4, bytes = bars + (2 * kPairStages + 3) * 8 + 16;
+};
+
+__device__ __forceinline__ bool wait_long(uint64_t* bar, unsigned parity, int64_t blocks) {
+    for (int64_t i = 0; i <= blocks / 64; ++i)
+        if (mbar_wait_bounded(bar, parity)) return true;
+    return false;
+}
+
+// Tile t of the walk: groups of kGroupM tile rows, column by column within a group.
+__device__ __forceinline__ void pair_tile(int64_t t, int64_t tiles_m, int64_t tiles_n, int64_t* tm, int64_t* tn) {
+    const int64_t group = t / (kGroupM * tiles_n), first = group * kGroupM;
+    const int64_t height = tiles_m - first < kGroupM ? tiles_m - first : kGroupM;
+    const int64_t in = t - group * kGroupM * tiles_n;
+    *tm = first + in % height;
+    *tn = in / height;
+}
+
+// 32 sums of row r from column c on, held by one thread.
+template <bool BF16OUT>
+__device__ __forceinline__ void store_row(const MatmulArgs& p, int64_t r, int64_t c, uint32_t (&v)[32]) {
+    if (p.mask) {
+        const uint32_t w = c < p.n ? __ldg(p.mask + r * p.wpr + c / 32) : 0u;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = (w >> i) & 1u ? v[i] : 0u;
+    }
+    if constexpr (BF16OUT) {
+        uint16_t* o = static_cast<uint16_t*>(p.out) + r * p.ldo + c;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[i])
+                    : "f"(__uint_as_float(v[16 * q + 2 * i + 1])), "f"(__uint_as_float(v[16 * q + 2 * i])));
+            if (c + 16 * q + 16 <= p.n) {
+                store32(o + 16 * q, h);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + 16 * q + i < p.n) o[16 * q + i] = uint16_t(i & 1 ? h[i / 2] >> 16 : h[i / 2] & 0xffffu);
+            }
+        }
+    } else {
+        float* o = static_cast<float*>(p.out) + r * p.ldo + c;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (c + 8 * q + 8 <= p.n) {
+                uint32_t h[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] = v[8 * q + i];
+                store32(o + 8 * q, h);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + 8 * q + i < p.n) o[8 * q + i] = __uint_as_float(v[8 * q + i]);
+            }
+        }
+    }
+}
+
+// The same for rows that do not start on 32 bytes: the warp's 32 x 32 sums turn
+// through shared memory, so that a store instruction covers one row.
+template <bool BF16OUT>
+__device__ __forceinline__ void store_turned(const MatmulArgs& p, int64_t r0, int64_t c, uint32_t (&v)[32], float* staged) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) staged[lane * 33 + i] = __uint_as_float(v[i]);
+    __syncwarp();
+    if (c + lane >= p.n) return;
+    for (int i = 0; i < 32 && r0 + i < p.m; ++i) {
+        float x = staged[i * 33 + lane];
+        const int64_t r = r0 + i;
+        if (p.mask && !((__ldg(p.mask + r * p.wpr + c / 32) >> lane) & 1u)) x = 0.f;
+        if constexpr (BF16OUT) static_cast<uint16_t*>(p.out)[r * p.ldo + c + lane] = to_bf16(x);
+        else static_cast<float*>(p.out)[r * p.ldo + c + lane] = x;
+    }
+}
+
+template <bool BF16OUT>
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+            const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb, const MatmulArgs p) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + PairSmem::bars);
+    uint64_t* empty = full + kPairStages;
+    uint64_t* ready = empty + kPairStages;       // an accumulator is complete (one barrier for each of the two)
+    uint64_t* room = ready + 2;                  // the next accumulator may be written
+    uint32_t* slot = reinterpret_cast<uint32_t*>(room + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned rank = cluster_rank();
+    const int64_t tiles_m = (p.m + kPairTile - 1) / kPairTile, tiles_n = (p.n + kPairTile - 1) / kPairTile;
+    const int64_t tiles = tiles_m * tiles_n, blocks = (p.k + kTile - 1) / kTile;
+    const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPairStages; ++i) {
+            mbar_init(full + i, 2);              // a producer of each CTA; used in the CTA of rank 0
+            mbar_init(empty + i, 1);
+        }
+        mbar_init(ready, 1);
+        mbar_init(ready + 1, 1);
+        mbar_init(room, 8);                      // the epilogue warps of both CTAs; used in rank 0
+        mbar_init_fence();
+    }
+    if (warp == 2) tmem_alloc<2>(slot, 512);
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tmem_fence_after();
+    const uint32_t tmem = *slot;
+    bool stalled = false;
+
+    if (warp == 0 && lane == 0) {
+        int st = 0;
+        unsigned phase = 0;
+        int64_t issued = 0;
+        for (int64_t t = first; t < tiles && !stalled; t += step) {
+            int64_t tm, tn;
+            pair_tile(t, tiles_m, tiles_n, &tm, &tn);
+            const int64_t a128 = tm * 2 + rank, b128 = tn * 2 + rank;
+            const int m = int(a128 * kTile), n = int(b128 * kTile);
+            for (int64_t kb = 0; kb < blocks; ++kb) {
+                if (!mbar_wait_bounded(empty + st, phase ^ 1)) { stalled = true; break; }
+                const uint32_t bar = cluster_addr(smem_u32(full + st), 0);
+                cluster_arrive_expect_tx(bar, 2 * kTileBytes + (kb % 4 == 0 ? 3 * kScaleBytes : 0));
+                const int k = int(kb * kTile);
+                tma_load_pair(smem + PairSmem::a + st * kTileBytes, &map_a, p.a_t ? m : k, p.a_t ? k : m, bar);
+                tma_load_pair(smem + PairSmem::b + st * kTileBytes, &map_b, p.b_t ? n : k, p.b_t ? k : n, bar);
+                if (kb % 4 == 0) {
+                    uint8_t* d = smem + PairSmem::s + st * 3 * kScaleBytes;
+                    tma_load_pair(d, &map_sa, 0, int((kb / 4) * p.tiles_m + a128), bar);
+                    tma_load_pair(d + kScaleBytes, &map_sb, 0, int((kb / 4) * p.tiles_n + tn * 2), bar);
+                }
+                ++issued;
+                if (++st == kPairStages) { st = 0; phase ^= 1; }
+            }
+        }
+        // copies in flight end before the pair does (rank 0's barriers count both CTAs' bytes)
+        if (stalled && rank == 0)
+            for (int i = 0; i < kPairStages && i < issued; ++i)
+                mbar_wait_bounded(full + i, unsigned((issued - 1 - i) / kPairStages) & 1);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        const uint32_t idesc = mma_desc(kPairTile, kPairTile, p.a_t, p.b_t);
+        const uint32_t step_a = (p.a_t ? 4096 : 32) >> 4, step_b = (p.b_t ? 4096 : 32) >> 4;
+        int st = 0;
+        unsigned phase = 0, n = 0;
+        for (int64_t t = first; t < tiles && !stalled; t += step, ++n) {
+            if (n > 0 && !mbar_wait_bounded(room, (n - 1) & 1)) { stalled = true; break; }
+            tmem_fence_after();
+            const uint32_t d = tmem + (n & 1 ? kSecond : 0);
+            for (int64_t kb = 0; kb < blocks; ++kb) {
+                if (!mbar_wait_bounded(full + st, phase)) { stalled = true; break; }
+                tmem_fence_after();
+                if (kb % 4 == 0) {
+                    const uint32_t s = smem_u32(smem + PairSmem::s + st * 3 * kScaleBytes);
+                    copy_scales<2>(tmem + kScaleA, scale_desc(s));
+                    copy_scales<2>(tmem + kScaleB, scale_desc(s + kScaleBytes));
+                    copy_scales<2>(tmem + kScaleB + 4, scale_desc(s + 2 * kScaleBytes));
+                }
+                const uint32_t id = with_scale_byte(idesc, uint32_t(kb % 4));
+                const uint64_t da = tile_desc(smem_u32(smem + PairSmem::a + st * kTileBytes), kTileBytes);
+                const uint64_t db = tile_desc(smem_u32(smem + PairSmem::b + st * kTileBytes), kTileBytes);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma_scaled<2>(d, da + i * step_a, db + i * step_b, id, tmem + kScaleA, tmem + kScaleB, kb > 0 || i > 0);
+                mma_commit_pair(empty + st);
+                if (++st == kPairStages) { st = 0; phase ^= 1; }
+            }
+            if (!stalled) mma_commit_pair(ready + (n & 1));
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp & 3;
+        float* staged = reinterpret_cast<float*>(smem + PairSmem::staged) + quarter * 32 * 33;
+        const uint32_t room_bar = cluster_addr(smem_u32(room), 0);
+        unsigned n = 0;
+        for (int64_t t = first; t < tiles; t += step, ++n) {
+            if (!wait_long(ready + (n & 1), (n >> 1) & 1, blocks)) { stalled = true; break; }
+            tmem_fence_after();
+            int64_t tm, tn;
+            pair_tile(t, tiles_m, tiles_n, &tm, &tn);
+            const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + (n & 1 ? kSecond : 0);
+            const int64_t r0 = (tm * 2 + rank) * kTile + quarter * 32, c0 = tn * kPairTile;
+#pragma unroll 1
+            for (int q = 0; q < 8; ++q) {
+                const int c = (n & 1 ? q : 7 - q) * 32;      // the columns that the other accumulator shares first
+                uint32_t v[32];
+                tmem_load32(d + c, v);
+                tmem_wait_load();
+                if (q == 0) {
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) cluster_arrive(room_bar);
+                }
+                if (c0 + c >= p.n) continue;
+                if (p.vec) {
+                    if (r0 + lane < p.m) store_row<BF16OUT>(p, r0 + lane, c0 + c, v);
+                } else {
+                    store_turned<BF16OUT>(p, r0, c0 + c, v, staged);
+                }
+            }
+        }
+    }
+    if (stalled) atomicAdd(&g_stalled, 1ull);
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();                              // both CTAs are done with each other's barriers and tensor memory
+    if (warp == 2) tmem_free<2>(tmem, 512);
+}
+
+// Tensor maps of the operands.
 PFN_cuTensorMapEncodeTiled g_encode = nullptr;
 std::once_flag g_encode_flag;
 
-cudaError_t encode_map(CUtensorMap* map, const uint8_t* v, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, const void* v, uint64_t inner, uint64_t outer,
+                   uint64_t stride, unsigned box_inner, unsigned box_outer, CUtensorMapSwizzle swizzle) {
     std::call_once(g_encode_flag, [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -233,14 +463,46 @@ cudaError_t encode_map(CUtensorMap* map, const uint8_t* v, int64_t rows, int64_t
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled>(fn);
     });
     if (!g_encode) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};      // columns past the matrix read as 0
-    const cuuint64_t strides[1] = {cuuint64_t(ld)};
-    const cuuint32_t box[2] = {kTile, cuuint32_t(box_rows)};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(v), dims, strides, box, estr,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t dims[2] = {inner, outer};               // what lies past the matrix reads as 0
+    const cuuint64_t strides[1] = {stride};
+    const cuuint32_t box[2] = {box_inner, box_outer}, estr[2] = {1, 1};
+    const CUresult r = g_encode(map, type, 2, const_cast<void*>(v), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// The codes of an operand whose tiles have `own` of its uncontracted and 128 of the
+// contracted axis: n x k codes, or k x n ones (t).
+cudaError_t encode_codes(CUtensorMap* map, const uint8_t* v, int64_t n, int64_t k, int64_t ld, bool t, int own) {
+    return t ? encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, v, n, k, ld, kTile, kTile, CU_TENSOR_MAP_SWIZZLE_128B)
+             : encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, v, k, n, ld, kTile, own, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Scale entries as rows of 128 words; `count` of them to a copy.  A copy past the last
+// tile of a block group brings the next group's entries, or zeros: scales of rows that do not exist.
+cudaError_t encode_scales(CUtensorMap* map, const uint8_t* s, int64_t tiles, int64_t k, int count) {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, s, 128, tiles * ((k + 511) / 512), kScaleBytes, 128, count,
+                  CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+cudaError_t launch_pair(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, cudaStream_t st) {
+    CUtensorMap map_a, map_b, map_sa, map_sb;
+    cudaError_t e = encode_codes(&map_a, a, p.m, p.k, lda, p.a_t, kTile);
+    if (e == cudaSuccess) e = encode_codes(&map_b, b, p.n, p.k, ldb, p.b_t, kTile);
+    if (e == cudaSuccess) e = encode_scales(&map_sa, p.sa, p.tiles_m, p.k, 1);
+    if (e == cudaSuccess) e = encode_scales(&map_sb, p.sb, p.tiles_n, p.k, 2);
+    if (e != cudaSuccess) return e;
+    const int64_t es = p.bf16 ? 2 : 4;
+    p.vec = aligned(p.out, 32) && p.ldo * es % 32 == 0;
+    const int64_t tiles = ((p.m + kPairTile - 1) / kPairTile) * ((p.n + kPairTile - 1) / kPairTile);
+    const unsigned grid = unsigned(tiles < 74 ? 2 * tiles : 148);
+    constexpr unsigned bytes = PairSmem::bytes + 1024;
+    static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
+    auto* kernel = p.bf16 ? pair_kernel<true> : pair_kernel<false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kPairThreads, bytes, st>>>(map_a, map_b, map_sa, map_sb, p);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_split(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, cudaStream_t st) {
@@ -248,8 +510,8 @@ cudaError_t launch_split(MatmulArgs p, const uint8_t* a, int64_t lda, const uint
     const int box_a = p.a_t || p.m >= kTile ? kTile : int((p.m + 7) / 8 * 8);
     p.a_bytes = box_a * kTile;
     CUtensorMap map_a, map_b;
-    cudaError_t e = p.a_t ? encode_map(&map_a, a, p.k, p.m, lda, kTile) : encode_map(&map_a, a, p.m, p.k, lda, box_a);
-    if (e == cudaSuccess) e = p.b_t ? encode_map(&map_b, b, p.k, p.n, ldb, kTile) : encode_map(&map_b, b, p.n, p.k, ldb, kTile);
+    cudaError_t e = encode_codes(&map_a, a, p.m, p.k, lda, p.a_t, box_a);
+    if (e == cudaSuccess) e = encode_codes(&map_b, b, p.n, p.k, ldb, p.b_t, kTile);
     if (e != cudaSuccess) return e;
     // two CTAs to an SM
     p.stages = (110 * 1024) / (p.a_bytes + kTileBytes + 2 * kScaleBytes);
@@ -326,6 +588,6 @@ extern "C" tsenor_status tsenor_matmul(tsenor_form form, const uint8_t* a, int64
     p.b_t = b_t;
     p.bf16 = dtype == TSENOR_BF16;
     p.vec = aligned(out, 4 * es) && ldo % 4 == 0;
-    const cudaError_t e = launch_split(p, a, lda, b, ldb, st);
+    const cudaError_t e = m > kTile ? launch_pair(p, a, lda, b, ldb, st) : launch_split(p, a, lda, b, ldb, st);
     return e == cudaSuccess ? TSENOR_OK : cuda_fail(e, "tsenor_matmul launch");
 }
