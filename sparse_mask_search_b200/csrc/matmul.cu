@@ -123,22 +123,25 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     const uint32_t tmem = *slot;
     bool stalled = false;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         int st = 0;
         unsigned phase = 0;
         int64_t issued = 0;
         for (int64_t kb = k0; kb < k1; ++kb) {
             if (!mbar_wait_bounded(empty + st, phase ^ 1)) { stalled = true; break; }
-            const bool scales = kb == k0 || kb % 4 == 0;
-            mbar_arrive_expect_tx(full + st, p.a_bytes + kTileBytes + (scales ? 2 * kScaleBytes : 0));
-            const int k = int(kb * kTile), m = int(tm * kTile), n = int(tn * kTile);
-            tma_load_2d(smem + at.a + st * p.a_bytes, &map_a, p.a_t ? m : k, p.a_t ? k : m, full + st);
-            tma_load_2d(smem + at.b + st * kTileBytes, &map_b, p.b_t ? n : k, p.b_t ? k : n, full + st);
-            if (scales) {
-                uint8_t* d = smem + at.s + st * 2 * kScaleBytes;
-                bulk_load(d, p.sa + ((kb / 4) * p.tiles_m + tm) * kScaleBytes, kScaleBytes, full + st);
-                bulk_load(d + kScaleBytes, p.sb + ((kb / 4) * p.tiles_n + tn) * kScaleBytes, kScaleBytes, full + st);
+            if (elect_one()) {
+                const bool scales = kb == k0 || kb % 4 == 0;
+                mbar_arrive_expect_tx(full + st, p.a_bytes + kTileBytes + (scales ? 2 * kScaleBytes : 0));
+                const int k = int(kb * kTile), m = int(tm * kTile), n = int(tn * kTile);
+                tma_load_2d(smem + at.a + st * p.a_bytes, &map_a, p.a_t ? m : k, p.a_t ? k : m, full + st);
+                tma_load_2d(smem + at.b + st * kTileBytes, &map_b, p.b_t ? n : k, p.b_t ? k : n, full + st);
+                if (scales) {
+                    uint8_t* d = smem + at.s + st * 2 * kScaleBytes;
+                    bulk_load(d, p.sa + ((kb / 4) * p.tiles_m + tm) * kScaleBytes, kScaleBytes, full + st);
+                    bulk_load(d + kScaleBytes, p.sb + ((kb / 4) * p.tiles_n + tn) * kScaleBytes, kScaleBytes, full + st);
+                }
             }
+            __syncwarp();
             ++issued;
             if (++st == p.stages) { st = 0; phase ^= 1; }
         }
@@ -146,7 +149,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         if (stalled)
             for (int i = 0; i < p.stages && i < issued; ++i)
                 mbar_wait_bounded(full + i, unsigned((issued - 1 - i) / p.stages) & 1);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         const uint32_t idesc = mma_desc(kTile, kTile, p.a_t, p.b_t);
         // 32 of the contracted axis: 32 bytes of a row, or 32 rows
         const uint32_t step_a = (p.a_t ? 4096 : 32) >> 4, step_b = (p.b_t ? 4096 : 32) >> 4;
@@ -156,21 +159,24 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         for (int64_t kb = k0; kb < k1; ++kb) {
             if (!mbar_wait_bounded(full + st, phase)) { stalled = true; break; }
             tmem_fence_after();
-            if (kb == k0 || kb % 4 == 0) {
-                const uint32_t s = smem_u32(smem + at.s + st * 2 * kScaleBytes);
-                copy_scales<1>(ts, scale_desc(s));
-                copy_scales<1>(ts + 4, scale_desc(s + kScaleBytes));
-            }
-            const uint32_t id = with_scale_byte(idesc, uint32_t(kb % 4));
-            const uint64_t da = tile_desc(smem_u32(smem + at.a + st * p.a_bytes), kTileBytes);
-            const uint64_t db = tile_desc(smem_u32(smem + at.b + st * kTileBytes), kTileBytes);
+            if (elect_one()) {
+                if (kb == k0 || kb % 4 == 0) {
+                    const uint32_t s = smem_u32(smem + at.s + st * 2 * kScaleBytes);
+                    copy_scales<1>(ts, scale_desc(s));
+                    copy_scales<1>(ts + 4, scale_desc(s + kScaleBytes));
+                }
+                const uint32_t id = with_scale_byte(idesc, uint32_t(kb % 4));
+                const uint64_t da = tile_desc(smem_u32(smem + at.a + st * p.a_bytes), kTileBytes);
+                const uint64_t db = tile_desc(smem_u32(smem + at.b + st * kTileBytes), kTileBytes);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                mma_scaled<1>(tmem, da + i * step_a, db + i * step_b, id, ts, ts + 4, kb > k0 || i > 0);
-            mma_commit(empty + st);
+                for (int i = 0; i < 4; ++i)
+                    mma_scaled<1>(tmem, da + i * step_a, db + i * step_b, id, ts, ts + 4, kb > k0 || i > 0);
+                mma_commit(empty + st);
+            }
+            __syncwarp();
             if (++st == p.stages) { st = 0; phase ^= 1; }
         }
-        if (k1 > k0) mma_commit(done);
+        if (k1 > k0 && elect_one()) mma_commit(done);
     }
     __syncwarp();
     // the sums of a share may take long: the wait's bound grows with their number
@@ -198,7 +204,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             }
         }
     }
-    if (stalled) atomicAdd(&g_stalled, 1ull);
+    if (stalled && lane == 0) atomicAdd(&g_stalled, 1ull);
     tmem_fence_before();
     __syncthreads();
     if (warp == 2) tmem_free<1>(tmem, kTmemCols);
@@ -335,7 +341,7 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPairStages; ++i) {
-            mbar_init(full + i, 2);              // a producer of each CTA; used in the CTA of rank 0
+            mbar_init(full + i, 1);              // used in the CTA of rank 0, which expects both CTAs' bytes
             mbar_init(empty + i, 1);
         }
         mbar_init(ready, 1);
@@ -351,7 +357,11 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     const uint32_t tmem = *slot;
     bool stalled = false;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
+        // A stage of rank 0's CTA is full when the bytes of both CTAs are there.  Rank 1's copies may
+        // count before rank 0 expects them: the stage was free in both CTAs, so its barrier is
+        // already in this phase, and the phase cannot end without rank 0's arrival.
+        const uint32_t full0 = cluster_addr(smem_u32(full), 0);
         int st = 0;
         unsigned phase = 0;
         int64_t issued = 0;
@@ -362,16 +372,19 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const int m = int(a128 * kTile), n = int(b128 * kTile);
             for (int64_t kb = 0; kb < blocks; ++kb) {
                 if (!mbar_wait_bounded(empty + st, phase ^ 1)) { stalled = true; break; }
-                const uint32_t bar = cluster_addr(smem_u32(full + st), 0);
-                cluster_arrive_expect_tx(bar, 2 * kTileBytes + (kb % 4 == 0 ? 3 * kScaleBytes : 0));
-                const int k = int(kb * kTile);
-                tma_load_pair(smem + PairSmem::a + st * kTileBytes, &map_a, p.a_t ? m : k, p.a_t ? k : m, bar);
-                tma_load_pair(smem + PairSmem::b + st * kTileBytes, &map_b, p.b_t ? n : k, p.b_t ? k : n, bar);
-                if (kb % 4 == 0) {
-                    uint8_t* d = smem + PairSmem::s + st * 3 * kScaleBytes;
-                    tma_load_pair(d, &map_sa, 0, int((kb / 4) * p.tiles_m + a128), bar);
-                    tma_load_pair(d + kScaleBytes, &map_sb, 0, int((kb / 4) * p.tiles_n + tn * 2), bar);
+                if (elect_one()) {
+                    const uint32_t bar = full0 + st * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(full + st, 4 * kTileBytes + (kb % 4 == 0 ? 6 * kScaleBytes : 0));
+                    const int k = int(kb * kTile);
+                    tma_load_pair(smem + PairSmem::a + st * kTileBytes, &map_a, p.a_t ? m : k, p.a_t ? k : m, bar);
+                    tma_load_pair(smem + PairSmem::b + st * kTileBytes, &map_b, p.b_t ? n : k, p.b_t ? k : n, bar);
+                    if (kb % 4 == 0) {
+                        uint8_t* d = smem + PairSmem::s + st * 3 * kScaleBytes;
+                        tma_load_pair(d, &map_sa, 0, int((kb / 4) * p.tiles_m + a128), bar);
+                        tma_load_pair(d + kScaleBytes, &map_sb, 0, int((kb / 4) * p.tiles_n + tn * 2), bar);
+                    }
                 }
+                __syncwarp();
                 ++issued;
                 if (++st == kPairStages) { st = 0; phase ^= 1; }
             }
@@ -380,7 +393,7 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         if (stalled && rank == 0)
             for (int i = 0; i < kPairStages && i < issued; ++i)
                 mbar_wait_bounded(full + i, unsigned((issued - 1 - i) / kPairStages) & 1);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         const uint32_t idesc = mma_desc(kPairTile, kPairTile, p.a_t, p.b_t);
         const uint32_t step_a = (p.a_t ? 4096 : 32) >> 4, step_b = (p.b_t ? 4096 : 32) >> 4;
         int st = 0;
@@ -392,22 +405,26 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             for (int64_t kb = 0; kb < blocks; ++kb) {
                 if (!mbar_wait_bounded(full + st, phase)) { stalled = true; break; }
                 tmem_fence_after();
-                if (kb % 4 == 0) {
-                    const uint32_t s = smem_u32(smem + PairSmem::s + st * 3 * kScaleBytes);
-                    copy_scales<2>(tmem + kScaleA, scale_desc(s));
-                    copy_scales<2>(tmem + kScaleB, scale_desc(s + kScaleBytes));
-                    copy_scales<2>(tmem + kScaleB + 4, scale_desc(s + 2 * kScaleBytes));
-                }
-                const uint32_t id = with_scale_byte(idesc, uint32_t(kb % 4));
-                const uint64_t da = tile_desc(smem_u32(smem + PairSmem::a + st * kTileBytes), kTileBytes);
-                const uint64_t db = tile_desc(smem_u32(smem + PairSmem::b + st * kTileBytes), kTileBytes);
+                if (elect_one()) {
+                    if (kb % 4 == 0) {
+                        const uint32_t s = smem_u32(smem + PairSmem::s + st * 3 * kScaleBytes);
+                        copy_scales<2>(tmem + kScaleA, scale_desc(s));
+                        copy_scales<2>(tmem + kScaleB, scale_desc(s + kScaleBytes));
+                        copy_scales<2>(tmem + kScaleB + 4, scale_desc(s + 2 * kScaleBytes));
+                    }
+                    const uint32_t id = with_scale_byte(idesc, uint32_t(kb % 4));
+                    const uint64_t da = tile_desc(smem_u32(smem + PairSmem::a + st * kTileBytes), kTileBytes);
+                    const uint64_t db = tile_desc(smem_u32(smem + PairSmem::b + st * kTileBytes), kTileBytes);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mma_scaled<2>(d, da + i * step_a, db + i * step_b, id, tmem + kScaleA, tmem + kScaleB, kb > 0 || i > 0);
-                mma_commit_pair(empty + st);
+                    for (int i = 0; i < 4; ++i)
+                        mma_scaled<2>(d, da + i * step_a, db + i * step_b, id, tmem + kScaleA, tmem + kScaleB, kb > 0 || i > 0);
+                    mma_commit_pair(empty + st);
+                }
+                __syncwarp();
                 if (++st == kPairStages) { st = 0; phase ^= 1; }
             }
-            if (!stalled) mma_commit_pair(ready + (n & 1));
+            if (!stalled && elect_one()) mma_commit_pair(ready + (n & 1));
+            __syncwarp();
         }
     } else if (warp >= 4) {
         const int quarter = warp & 3;
@@ -441,7 +458,7 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             }
         }
     }
-    if (stalled) atomicAdd(&g_stalled, 1ull);
+    if (stalled && lane == 0) atomicAdd(&g_stalled, 1ull);
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
