@@ -349,8 +349,8 @@ def _dense(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {shape}")
 
 
 def _mask_pointer(mask, rows, cols, device):
@@ -374,7 +374,9 @@ def _on(device, stream):
 def _launch(fn, device, *args):
     """fn(*args, stream) on the device's current stream."""
     import torch
-    _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if status:
+        _check(status)
 
 
 def _needs_guard(device, stream):
@@ -385,17 +387,19 @@ def _needs_guard(device, stream):
 def _new_codes(rows, cols, device):
     import torch
     ld = (cols + 15) // 16 * 16
-    return torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device)[:, :cols]
+    t = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device)
+    return t if ld == cols else t[:, :cols]
 
 
-def _codes(t, name, rows, cols, device):
+def _codes(t, name, device, shape=None):
     """(pointer, row stride) of a codes tensor."""
     import torch
     ld = _strided(t, name, (torch.float8_e4m3fn,))
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {(rows, cols)}")
     if rows <= 1 or cols == 0:
         ld = (cols + 15) // 16 * 16
     if ld % 16 or t.data_ptr() % 16:
@@ -430,18 +434,20 @@ def tsenor_quantize(X, block: str = "row", mask=None, out=None, stream=None):
         with _on(X.device, stream):
             return tsenor_quantize(X, block, mask, out)
     rows, cols = X.shape
-    mask_ptr = _mask_pointer(mask, rows, cols, X.device)
+    device = X.device
+    mask_ptr = _mask_pointer(mask, rows, cols, device)
     if out is None:
-        out = QuantizedMatrix(_new_codes(rows, cols, X.device),
-                              _new_scales(rows, cols, X.device) if block != "column" else None,
-                              _new_scales(cols, rows, X.device) if block != "row" else None)
+        out = QuantizedMatrix(_new_codes(rows, cols, device),
+                              _new_scales(rows, cols, device) if block != "column" else None,
+                              _new_scales(cols, rows, device) if block != "row" else None)
+        values, ldv = out.values.data_ptr(), (cols + 15) // 16 * 16
     else:
+        values, ldv = _codes(out.values, "out.values", device, (rows, cols))
         if block != "column":
-            _dense(out.scales, "out.scales", torch.uint8, scale_shape(rows, cols), X.device)
+            _dense(out.scales, "out.scales", torch.uint8, scale_shape(rows, cols), device)
         if block != "row":
-            _dense(out.scales_t, "out.scales_t", torch.uint8, scale_shape(cols, rows), X.device)
-    values, ldv = _codes(out.values, "out.values", rows, cols, X.device)
-    _launch(lib().tsenor_quantize, X.device, X.data_ptr(), _dtype_code(X), rows, cols, ldx, BLOCKS[block], mask_ptr,
+            _dense(out.scales_t, "out.scales_t", torch.uint8, scale_shape(cols, rows), device)
+    _launch(lib().tsenor_quantize, device, X.data_ptr(), _dtype_code(X), rows, cols, ldx, BLOCKS[block], mask_ptr,
             values, ldv, out.scales.data_ptr() if block != "column" else None,
             out.scales_t.data_ptr() if block != "row" else None)
     return out
@@ -517,13 +523,13 @@ def tsenor_matmul(A, B, form: str = "nt", mask=None, dtype=None, out=None, strea
     if _needs_guard(device, stream):
         with _on(device, stream):
             return tsenor_matmul(A, B, form, mask, dtype, out)
-    (ra, ca), (rb, cb) = A.shape, B.shape
+    a, lda = _codes(A.values, "A.values", device)
+    b, ldb = _codes(B.values, "B.values", device)
+    (ra, ca), (rb, cb) = A.values.shape, B.values.shape
     m, k = (ca, ra) if form == "tn" else (ra, ca)
     n, kb = (rb, cb) if form == "nt" else (cb, rb)
     if k != kb:
         raise ValueError(f"the operands sum over {k} and {kb} entries")
-    a, lda = _codes(A.values, "A.values", ra, ca, device)
-    b, ldb = _codes(B.values, "B.values", rb, cb, device)
     sa, sb = (A.scales_t if form == "tn" else A.scales), (B.scales if form == "nt" else B.scales_t)
     if sa is None or sb is None:
         raise ValueError(f'form "{form}" needs {"A.scales_t" if form == "tn" else "A.scales"} and '
