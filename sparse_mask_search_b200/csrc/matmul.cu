@@ -33,6 +33,8 @@ constexpr int kTile = 128;                       // rows, columns and summed ent
 constexpr int kTileBytes = kTile * kTile;
 constexpr int kScaleBytes = 512;
 constexpr int kThreads = 128;
+constexpr int kSms = 148;
+constexpr int kSplitStageBytes = 208 * 1024;     // of the stages of split_kernel: one CTA to an SM
 constexpr int kTmemCols = 256;                   // 128 of the accumulator, 4 of each side's scales
 constexpr int kPad = 132;                        // floats to a staged row: 16-byte stores without bank conflicts
 
@@ -116,14 +118,10 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         mbar_init(done, 1);
         mbar_init_fence();
     }
-    if (warp == 2) tmem_alloc<1>(slot, kTmemCols);
-    tmem_fence_before();
     __syncthreads();
-    tmem_fence_after();
-    const uint32_t tmem = *slot;
     bool stalled = false;
 
-    if (warp == 0) {
+    if (warp == 0) {                             // loads start while warp 1 gets its tensor memory
         int st = 0;
         unsigned phase = 0;
         int64_t issued = 0;
@@ -153,7 +151,8 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const uint32_t idesc = mma_desc(kTile, kTile, p.a_t, p.b_t);
         // 32 of the contracted axis: 32 bytes of a row, or 32 rows
         const uint32_t step_a = (p.a_t ? 4096 : 32) >> 4, step_b = (p.b_t ? 4096 : 32) >> 4;
-        const uint32_t ts = tmem + kTile;
+        tmem_alloc<1>(slot, kTmemCols);
+        const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(slot), ts = tmem + kTile;
         int st = 0;
         unsigned phase = 0;
         for (int64_t kb = k0; kb < k1; ++kb) {
@@ -178,7 +177,10 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         }
         if (k1 > k0 && elect_one()) mma_commit(done);
     }
-    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = *slot;
     // the sums of a share may take long: the wait's bound grows with their number
     bool ready = k1 == k0;
     for (int64_t i = 0; i <= (k1 - k0) / 64 && !ready; ++i) ready = mbar_wait_bounded(done, 0);
@@ -207,7 +209,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     if (stalled && lane == 0) atomicAdd(&g_stalled, 1ull);
     tmem_fence_before();
     __syncthreads();
-    if (warp == 2) tmem_free<1>(tmem, kTmemCols);
+    if (warp == 1) tmem_free<1>(tmem, kTmemCols);
     if (split > 1) cluster_sync();
     const uint32_t base = smem_u32(staged);
     for (int u = int(rank) * kThreads + threadIdx.x; u < rows * (kTile / 4); u += split * kThreads) {
@@ -512,7 +514,7 @@ cudaError_t launch_pair(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8
     const int64_t es = p.bf16 ? 2 : 4;
     p.vec = aligned(p.out, 32) && p.ldo * es % 32 == 0;
     const int64_t tiles = ((p.m + kPairTile - 1) / kPairTile) * ((p.n + kPairTile - 1) / kPairTile);
-    const unsigned grid = unsigned(tiles < 74 ? 2 * tiles : 148);
+    const unsigned grid = unsigned(tiles < kSms / 2 ? 2 * tiles : kSms);
     constexpr unsigned bytes = PairSmem::bytes + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     auto* kernel = p.bf16 ? pair_kernel<true> : pair_kernel<false>;
@@ -520,6 +522,14 @@ cudaError_t launch_pair(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8
     if (e != cudaSuccess) return e;
     kernel<<<grid, kPairThreads, bytes, st>>>(map_a, map_b, map_sa, map_sb, p);
     return cudaGetLastError();
+}
+
+// CTAs that share a tile's sum: as many as leave no SM with two (a kernel that
+// holds tensor memory runs one CTA to an SM), with two blocks of 128 each at least.
+int split_of(int64_t tiles, int64_t blocks) {
+    int split = 1;
+    while (split < 8 && tiles * (split + 1) <= kSms && blocks / (split + 1) >= 2) ++split;
+    return split;
 }
 
 cudaError_t launch_split(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, cudaStream_t st) {
@@ -530,11 +540,9 @@ cudaError_t launch_split(MatmulArgs p, const uint8_t* a, int64_t lda, const uint
     cudaError_t e = encode_codes(&map_a, a, p.m, p.k, lda, p.a_t, box_a);
     if (e == cudaSuccess) e = encode_codes(&map_b, b, p.n, p.k, ldb, p.b_t, kTile);
     if (e != cudaSuccess) return e;
-    // two CTAs to an SM
-    p.stages = (110 * 1024) / (p.a_bytes + kTileBytes + 2 * kScaleBytes);
+    p.stages = kSplitStageBytes / (p.a_bytes + kTileBytes + 2 * kScaleBytes);
     const int64_t tiles = p.tiles_m * p.tiles_n, blocks = (p.k + kTile - 1) / kTile;
-    int split = 1;
-    while (split < 8 && tiles * split < 148 && blocks / (2 * split) >= 2) split *= 2;
+    const int split = split_of(tiles, blocks);
     const unsigned bytes = SplitSmem(p.stages, p.a_bytes).bytes(p.stages) + 1024;
     e = cudaFuncSetAttribute(split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
