@@ -24,7 +24,7 @@ struct MatmulArgs {
     int stages;
     bool a_t, b_t;              // the operand is stored with its contracted axis along rows
     bool bf16;
-    bool vec;                   // four outputs of a row can be stored at once
+    bool vec;                   // rows of the output are aligned to the kernel's vector stores
 };
 
 __device__ unsigned long long g_stalled;
@@ -32,28 +32,15 @@ __device__ unsigned long long g_stalled;
 constexpr int kTile = 128;                       // rows, columns and summed entries of a tile
 constexpr int kTileBytes = kTile * kTile;
 constexpr int kScaleBytes = 512;
-constexpr int kThreads = 128;
 constexpr int kSms = 148;
-constexpr int kSplitStageBytes = 208 * 1024;     // of the stages of split_kernel: one CTA to an SM
-constexpr int kTmemCols = 256;                   // 128 of the accumulator, 4 of each side's scales
 constexpr int kPad = 132;                        // floats to a staged row: 16-byte stores without bank conflicts
 
-// Shared memory of split_kernel from its 1024-byte aligned base: the A tiles (which may be shorter than 128
-// rows: the rows behind them are read by the tensor core and go to rows of the
-// accumulator that nothing reads), the B tiles, the scales, the barriers.  The
-// fp32 accumulators are staged over the tiles at the end.
-struct SplitSmem {
-    unsigned a, b, s, bars;
-    __host__ __device__ SplitSmem(int stages, int a_bytes) {
-        a = 0;
-        b = stages * a_bytes;
-        s = b + stages * kTileBytes;
-        bars = s + stages * 2 * kScaleBytes;
-        const unsigned staged = kTile * kPad * 4;
-        if (bars < staged) bars = staged;
-    }
-    __host__ __device__ unsigned bytes(int stages) const { return bars + (2 * stages + 1) * 8 + 16; }
-};
+// The products issue and load loops may wait for as long as a tile's sums take.
+__device__ __forceinline__ bool wait_long(uint64_t* bar, unsigned parity, int64_t blocks) {
+    for (int64_t i = 0; i <= blocks / 64; ++i)
+        if (mbar_wait_bounded(bar, parity)) return true;
+    return false;
+}
 
 __device__ __forceinline__ uint16_t to_bf16(float x) {
     uint16_t h;
@@ -62,6 +49,7 @@ __device__ __forceinline__ uint16_t to_bf16(float x) {
 }
 
 // Four sums of row r from column c on: mask, rounding, store.
+template <bool BF16OUT>
 __device__ __forceinline__ void store4(const MatmulArgs& p, int64_t r, int64_t c, float4 v) {
     float x[4] = {v.x, v.y, v.z, v.w};
     if (p.mask) {
@@ -69,7 +57,7 @@ __device__ __forceinline__ void store4(const MatmulArgs& p, int64_t r, int64_t c
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = (w >> i) & 1u ? x[i] : 0.f;
     }
-    if (p.bf16) {
+    if constexpr (BF16OUT) {
         uint16_t* o = static_cast<uint16_t*>(p.out) + r * p.ldo + c;
         if (p.vec && c + 4 <= p.n) {
             *reinterpret_cast<uint2*>(o) = make_uint2(to_bf16(x[0]) | (uint32_t(to_bf16(x[1])) << 16),
@@ -87,179 +75,6 @@ __device__ __forceinline__ void store4(const MatmulArgs& p, int64_t r, int64_t c
                 if (c + i < p.n) o[i] = x[i];
         }
     }
-}
-
-// One 128 x 128 tile of the output to a cluster of `split` CTAs; each sums its
-// share of the blocks of 128 in its tensor memory, and the shares are added in
-// rank order through distributed shared memory.  Warp 0 loads (TMA, a ring of
-// stages), warp 1 issues the products, all four warps store.
-__global__ void __launch_bounds__(kThreads)
-split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const MatmulArgs p,
-             const int split) {
-    extern __shared__ uint8_t raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const SplitSmem at(p.stages, p.a_bytes);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + at.bars);
-    uint64_t* empty = full + p.stages;
-    uint64_t* done = empty + p.stages;
-    uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const unsigned rank = split > 1 ? cluster_rank() : 0;
-    const int64_t tile = blockIdx.x / split;
-    const int64_t tm = tile % p.tiles_m, tn = tile / p.tiles_m;
-    const int64_t blocks = (p.k + kTile - 1) / kTile;
-    const int64_t k0 = blocks * rank / split, k1 = blocks * (rank + 1) / split;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < p.stages; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, 1);
-        }
-        mbar_init(done, 1);
-        mbar_init_fence();
-    }
-    __syncthreads();
-    bool stalled = false;
-
-    if (warp == 0) {                             // loads start while warp 1 gets its tensor memory
-        int st = 0;
-        unsigned phase = 0;
-        int64_t issued = 0;
-        for (int64_t kb = k0; kb < k1; ++kb) {
-            if (!mbar_wait_bounded(empty + st, phase ^ 1)) { stalled = true; break; }
-            if (elect_one()) {
-                const bool scales = kb == k0 || kb % 4 == 0;
-                mbar_arrive_expect_tx(full + st, p.a_bytes + kTileBytes + (scales ? 2 * kScaleBytes : 0));
-                const int k = int(kb * kTile), m = int(tm * kTile), n = int(tn * kTile);
-                tma_load_2d(smem + at.a + st * p.a_bytes, &map_a, p.a_t ? m : k, p.a_t ? k : m, full + st);
-                tma_load_2d(smem + at.b + st * kTileBytes, &map_b, p.b_t ? n : k, p.b_t ? k : n, full + st);
-                if (scales) {
-                    uint8_t* d = smem + at.s + st * 2 * kScaleBytes;
-                    bulk_load(d, p.sa + ((kb / 4) * p.tiles_m + tm) * kScaleBytes, kScaleBytes, full + st);
-                    bulk_load(d + kScaleBytes, p.sb + ((kb / 4) * p.tiles_n + tn) * kScaleBytes, kScaleBytes, full + st);
-                }
-            }
-            __syncwarp();
-            ++issued;
-            if (++st == p.stages) { st = 0; phase ^= 1; }
-        }
-        // copies in flight end before the block does
-        if (stalled)
-            for (int i = 0; i < p.stages && i < issued; ++i)
-                mbar_wait_bounded(full + i, unsigned((issued - 1 - i) / p.stages) & 1);
-    } else if (warp == 1) {
-        const uint32_t idesc = mma_desc(kTile, kTile, p.a_t, p.b_t);
-        // 32 of the contracted axis: 32 bytes of a row, or 32 rows
-        const uint32_t step_a = (p.a_t ? 4096 : 32) >> 4, step_b = (p.b_t ? 4096 : 32) >> 4;
-        tmem_alloc<1>(slot, kTmemCols);
-        const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(slot), ts = tmem + kTile;
-        int st = 0;
-        unsigned phase = 0;
-        for (int64_t kb = k0; kb < k1; ++kb) {
-            if (!mbar_wait_bounded(full + st, phase)) { stalled = true; break; }
-            tmem_fence_after();
-            if (elect_one()) {
-                if (kb == k0 || kb % 4 == 0) {
-                    const uint32_t s = smem_u32(smem + at.s + st * 2 * kScaleBytes);
-                    copy_scales<1>(ts, scale_desc(s));
-                    copy_scales<1>(ts + 4, scale_desc(s + kScaleBytes));
-                }
-                const uint32_t id = with_scale_byte(idesc, uint32_t(kb % 4));
-                const uint64_t da = tile_desc(smem_u32(smem + at.a + st * p.a_bytes), kTileBytes);
-                const uint64_t db = tile_desc(smem_u32(smem + at.b + st * kTileBytes), kTileBytes);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mma_scaled<1>(tmem, da + i * step_a, db + i * step_b, id, ts, ts + 4, kb > k0 || i > 0);
-                mma_commit(empty + st);
-            }
-            __syncwarp();
-            if (++st == p.stages) { st = 0; phase ^= 1; }
-        }
-        if (k1 > k0 && elect_one()) mma_commit(done);
-    }
-    tmem_fence_before();
-    __syncthreads();
-    tmem_fence_after();
-    const uint32_t tmem = *slot;
-    // the sums of a share may take long: the wait's bound grows with their number
-    bool ready = k1 == k0;
-    for (int64_t i = 0; i <= (k1 - k0) / 64 && !ready; ++i) ready = mbar_wait_bounded(done, 0);
-    if (!ready) stalled = true;
-    tmem_fence_after();
-
-    const int64_t rows = p.m - tm * kTile < kTile ? p.m - tm * kTile : kTile;
-    float* staged = reinterpret_cast<float*>(smem);
-    {
-        const int r = warp * 32 + lane;
-        if (warp * 32 < rows) {
-#pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
-                uint32_t v[32];
-                tmem_load32(tmem + (uint32_t(warp * 32) << 16) + c, v);
-                tmem_wait_load();
-                if (r < rows) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<uint4*>(staged + r * kPad + c + i) =
-                            k1 > k0 ? make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_uint4(0, 0, 0, 0);
-                }
-            }
-        }
-    }
-    if (stalled && lane == 0) atomicAdd(&g_stalled, 1ull);
-    tmem_fence_before();
-    __syncthreads();
-    if (warp == 1) tmem_free<1>(tmem, kTmemCols);
-    if (split > 1) cluster_sync();
-    const uint32_t base = smem_u32(staged);
-    for (int u = int(rank) * kThreads + threadIdx.x; u < rows * (kTile / 4); u += split * kThreads) {
-        const int r = u / (kTile / 4), c = u % (kTile / 4) * 4;
-        if (tn * kTile + c >= p.n) continue;
-        float4 v = *reinterpret_cast<const float4*>(staged + r * kPad + c);
-        if (split > 1) {
-            v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int q = 0; q < split; ++q) {
-                const float4 w = cluster_load4(cluster_addr(base + (r * kPad + c) * 4, q));
-                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-            }
-        }
-        store4(p, tm * kTile + r, tn * kTile + c, v);
-    }
-    if (split > 1) cluster_sync();               // a peer's shared memory lives until all have read it
-}
-
-// ---- large products -------------------------------------------------------------------
-//
-// A pair of CTAs works on a 256 x 256 tile (cta_group::2): each holds 128 rows of
-// A and 128 of B in shared memory and 128 rows of the accumulator.  The pairs are
-// persistent.  Two accumulators of 256 columns and the scales do not fit into
-// 512 columns of tensor memory, so the second one starts at column 240: its
-// product may start once the 32 columns that hold the overlap have been read, which
-// the epilogue does first.
-constexpr int kPairThreads = 256;                // warps: 0 loads, 1 products, 2 tensor memory, 4-7 epilogue
-constexpr int kPairTile = 256;
-constexpr int kPairStages = 6;
-constexpr int kSecond = 240, kScaleA = 496, kScaleB = 500;
-constexpr int kGroupM = 16;                      // tiles of 256 rows walked together, so that B is read from L2
-
-struct PairSmem {
-    static constexpr unsigned a = 0, b = kPairStages * kTileBytes, s = 2 * b, staged = s + kPairStages * 3 * kScaleBytes,
-                              bars = staged + 4 * 32 * 33 * 4, bytes = bars + (2 * kPairStages + 3) * 8 + 16;
-};
-
-__device__ __forceinline__ bool wait_long(uint64_t* bar, unsigned parity, int64_t blocks) {
-    for (int64_t i = 0; i <= blocks / 64; ++i)
-        if (mbar_wait_bounded(bar, parity)) return true;
-    return false;
-}
-
-// Tile t of the walk: groups of kGroupM tile rows, column by column within a group.
-__device__ __forceinline__ void pair_tile(int64_t t, int64_t tiles_m, int64_t tiles_n, int64_t* tm, int64_t* tn) {
-    const int64_t group = t / (kGroupM * tiles_n), first = group * kGroupM;
-    const int64_t height = tiles_m - first < kGroupM ? tiles_m - first : kGroupM;
-    const int64_t in = t - group * kGroupM * tiles_n;
-    *tm = first + in % height;
-    *tn = in / height;
 }
 
 // 32 sums of row r from column c on, held by one thread.
@@ -322,6 +137,223 @@ __device__ __forceinline__ void store_turned(const MatmulArgs& p, int64_t r0, in
         if constexpr (BF16OUT) static_cast<uint16_t*>(p.out)[r * p.ldo + c + lane] = to_bf16(x);
         else static_cast<float*>(p.out)[r * p.ldo + c + lane] = x;
     }
+}
+
+// ---- few rows, or few tiles --------------------------------------------------------------
+//
+// 128 x 128 tiles.  Warp 0 loads (TMA, a ring of stages), warp 1 issues the products,
+// warps 2 to 5 store.  A kernel that holds tensor memory runs one CTA to an SM, so a CTA takes all
+// of its shared memory: what bounds a product of few rows is the bytes of B in flight.
+//
+// SPLIT: a tile belongs to a cluster of `split` CTAs; each sums its share of the blocks
+// of 128, and the shares are added in rank order through distributed shared memory.
+// Otherwise the CTAs are persistent and walk the tiles, with two accumulators, so that the
+// loads of the next tile never wait for a store.
+constexpr int kThreads = 192;
+constexpr int kTmemCols = 512;                   // two accumulators of 128, 4 columns of each side's scales
+constexpr int kStageBytes = 224 * 1024;          // of all stages and the room to turn
+
+// Shared memory from its 1024-byte aligned base: the A tiles (which may be shorter than
+// 128 rows: the rows behind them are read by the tensor core and go to rows of the
+// accumulator that nothing reads), the B tiles, the scales, room to turn 32 x 32 sums, the barriers.
+// The shares of a split tile are staged over the tiles at the end.
+struct TileSmem {
+    unsigned a, b, s, turn, bars;
+    __host__ __device__ TileSmem(int stages, int a_bytes) {
+        a = 0;
+        b = stages * a_bytes;
+        s = b + stages * kTileBytes;
+        turn = s + stages * 2 * kScaleBytes;
+        bars = turn + 4 * 32 * 33 * 4;
+    }
+    __host__ __device__ unsigned bytes(int stages) const { return bars + (2 * stages + 4) * 8 + 16; }
+};
+
+template <bool SPLIT, bool BF16OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const MatmulArgs p,
+            const int split) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const TileSmem at(p.stages, p.a_bytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + at.bars);
+    uint64_t* empty = full + p.stages;
+    uint64_t* ready = empty + p.stages;          // an accumulator is complete
+    uint64_t* room = ready + 2;                  // an accumulator has been read
+    uint32_t* slot = reinterpret_cast<uint32_t*>(room + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned rank = SPLIT ? cluster_rank() : 0;
+    const int64_t tiles = p.tiles_m * p.tiles_n, blocks = (p.k + kTile - 1) / kTile;
+    const int64_t first = SPLIT ? blockIdx.x / split : blockIdx.x, step = SPLIT ? tiles : gridDim.x;
+    const int64_t k0 = SPLIT ? blocks * rank / split : 0, k1 = SPLIT ? blocks * (rank + 1) / split : blocks;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(ready + i, 1);
+            mbar_init(room + i, 4);
+        }
+        mbar_init_fence();
+    }
+    __syncthreads();
+    bool stalled = false;
+
+    if (warp == 0) {                             // loads start while warp 1 gets its tensor memory
+        int st = 0;
+        unsigned phase = 0;
+        int64_t issued = 0;
+        for (int64_t t = first; t < tiles && !stalled; t += step) {
+            const int64_t tm = t % p.tiles_m, tn = t / p.tiles_m;
+            const int m = int(tm * kTile), n = int(tn * kTile);
+            for (int64_t kb = k0; kb < k1; ++kb) {
+                if (!mbar_wait_bounded(empty + st, phase ^ 1)) { stalled = true; break; }
+                if (elect_one()) {
+                    const bool scales = kb == k0 || kb % 4 == 0;
+                    mbar_arrive_expect_tx(full + st, p.a_bytes + kTileBytes + (scales ? 2 * kScaleBytes : 0));
+                    const int k = int(kb * kTile);
+                    tma_load_2d(smem + at.a + st * p.a_bytes, &map_a, p.a_t ? m : k, p.a_t ? k : m, full + st);
+                    tma_load_2d(smem + at.b + st * kTileBytes, &map_b, p.b_t ? n : k, p.b_t ? k : n, full + st);
+                    if (scales) {
+                        uint8_t* d = smem + at.s + st * 2 * kScaleBytes;
+                        bulk_load(d, p.sa + ((kb / 4) * p.tiles_m + tm) * kScaleBytes, kScaleBytes, full + st);
+                        bulk_load(d + kScaleBytes, p.sb + ((kb / 4) * p.tiles_n + tn) * kScaleBytes, kScaleBytes, full + st);
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++st == p.stages) { st = 0; phase ^= 1; }
+            }
+        }
+        // copies in flight end before the block does
+        if (stalled)
+            for (int i = 0; i < p.stages && i < issued; ++i)
+                mbar_wait_bounded(full + i, unsigned((issued - 1 - i) / p.stages) & 1);
+    } else if (warp == 1) {
+        const uint32_t idesc = mma_desc(kTile, kTile, p.a_t, p.b_t);
+        // 32 of the contracted axis: 32 bytes of a row, or 32 rows
+        const uint32_t step_a = (p.a_t ? 4096 : 32) >> 4, step_b = (p.b_t ? 4096 : 32) >> 4;
+        tmem_alloc<1>(slot, kTmemCols);
+        const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(slot), ts = tmem + 2 * kTile;
+        int st = 0;
+        unsigned phase = 0, n = 0;
+        for (int64_t t = first; t < tiles && !stalled; t += step, ++n) {
+            if (n > 1 && !mbar_wait_bounded(room + (n & 1), ((n >> 1) - 1) & 1)) { stalled = true; break; }
+            tmem_fence_after();
+            const uint32_t d = tmem + (n & 1) * kTile;
+            for (int64_t kb = k0; kb < k1; ++kb) {
+                if (!mbar_wait_bounded(full + st, phase)) { stalled = true; break; }
+                tmem_fence_after();
+                if (elect_one()) {
+                    if (kb == k0 || kb % 4 == 0) {
+                        const uint32_t s = smem_u32(smem + at.s + st * 2 * kScaleBytes);
+                        copy_scales<1>(ts, scale_desc(s));
+                        copy_scales<1>(ts + 4, scale_desc(s + kScaleBytes));
+                    }
+                    const uint32_t id = with_scale_byte(idesc, uint32_t(kb % 4));
+                    const uint64_t da = tile_desc(smem_u32(smem + at.a + st * p.a_bytes), kTileBytes);
+                    const uint64_t db = tile_desc(smem_u32(smem + at.b + st * kTileBytes), kTileBytes);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma_scaled<1>(d, da + i * step_a, db + i * step_b, id, ts, ts + 4, kb > k0 || i > 0);
+                    mma_commit(empty + st);
+                }
+                __syncwarp();
+                if (++st == p.stages) { st = 0; phase ^= 1; }
+            }
+            if (!stalled && elect_one()) mma_commit(ready + (n & 1));
+            __syncwarp();
+        }
+    } else {
+        const int quarter = warp & 3;            // the lanes of tensor memory that a warp may read
+        float* turn = reinterpret_cast<float*>(smem + at.turn) + quarter * 32 * 33;
+        float* staged = reinterpret_cast<float*>(smem);
+        unsigned n = 0;
+        for (int64_t t = first; t < tiles; t += step, ++n) {
+            if (!wait_long(ready + (n & 1), (n >> 1) & 1, k1 - k0)) { stalled = true; break; }
+            tmem_fence_after();
+            const int64_t r0 = t % p.tiles_m * kTile + quarter * 32, c0 = t / p.tiles_m * kTile;
+            const uint32_t d = *reinterpret_cast<volatile uint32_t*>(slot) + (uint32_t(quarter * 32) << 16) + (n & 1) * kTile;
+            if (r0 < p.m) {
+#pragma unroll 1
+                for (int c = 0; c < kTile; c += 32) {
+                    uint32_t v[32];
+                    tmem_load32(d + c, v);
+                    tmem_wait_load();
+                    if constexpr (SPLIT) {
+                        if (r0 + lane < p.m) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *reinterpret_cast<uint4*>(staged + (quarter * 32 + lane) * kPad + c + i) =
+                                    make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        }
+                    } else if (c0 + c < p.n) {
+                        if (p.vec) {
+                            if (r0 + lane < p.m) store_row<BF16OUT>(p, r0 + lane, c0 + c, v);
+                        } else {
+                            store_turned<BF16OUT>(p, r0, c0 + c, v, turn);
+                        }
+                    }
+                }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(room + (n & 1));
+        }
+    }
+    if (stalled && lane == 0) atomicAdd(&g_stalled, 1ull);
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 1) tmem_free<1>(*slot, kTmemCols);
+    if constexpr (SPLIT) {
+        cluster_sync();
+        const int64_t tm = first % p.tiles_m, tn = first / p.tiles_m;
+        const int rows = int(p.m - tm * kTile < kTile ? p.m - tm * kTile : kTile);
+        const uint32_t base = smem_u32(smem);
+        for (int u = int(rank) * kThreads + threadIdx.x; u < rows * (kTile / 4); u += split * kThreads) {
+            const int r = u / (kTile / 4), c = u % (kTile / 4) * 4;
+            if (tn * kTile + c >= p.n) continue;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int q = 0; q < split; ++q) {
+                const float4 w = cluster_load4(cluster_addr(base + (r * kPad + c) * 4, q));
+                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+            }
+            store4<BF16OUT>(p, tm * kTile + r, tn * kTile + c, v);
+        }
+        cluster_sync();                          // a peer's shared memory lives until all have read it
+    }
+}
+
+// ---- large products -------------------------------------------------------------------
+//
+// A pair of CTAs works on a 256 x 256 tile (cta_group::2): each holds 128 rows of
+// A and 128 of B in shared memory and 128 rows of the accumulator.  The pairs are
+// persistent.  Two accumulators of 256 columns and the scales do not fit into
+// 512 columns of tensor memory, so the second one starts at column 240: its
+// product may start once the 32 columns that hold the overlap have been read, which
+// the epilogue does first.
+constexpr int kPairThreads = 256;                // warps: 0 loads, 1 products, 2 tensor memory, 4-7 epilogue
+constexpr int kPairTile = 256;
+constexpr int kPairStages = 6;
+constexpr int kSecond = 240, kScaleA = 496, kScaleB = 500;
+constexpr int kGroupM = 16;                      // tiles of 256 rows walked together, so that B is read from L2
+
+struct PairSmem {
+    static constexpr unsigned a = 0, b = kPairStages * kTileBytes, s = 2 * b, staged = s + kPairStages * 3 * kScaleBytes,
+                              bars = staged + 4 * 32 * 33 * 4, bytes = bars + (2 * kPairStages + 3) * 8 + 16;
+};
+
+// Tile t of the walk: groups of kGroupM tile rows, column by column within a group.
+__device__ __forceinline__ void pair_tile(int64_t t, int64_t tiles_m, int64_t tiles_n, int64_t* tm, int64_t* tn) {
+    const int64_t group = t / (kGroupM * tiles_n), first = group * kGroupM;
+    const int64_t height = tiles_m - first < kGroupM ? tiles_m - first : kGroupM;
+    const int64_t in = t - group * kGroupM * tiles_n;
+    *tm = first + in % height;
+    *tn = in / height;
 }
 
 template <bool BF16OUT>
@@ -532,7 +564,9 @@ int split_of(int64_t tiles, int64_t blocks) {
     return split;
 }
 
-cudaError_t launch_split(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, cudaStream_t st) {
+template <bool SPLIT>
+cudaError_t launch_tiles(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int split,
+                         cudaStream_t st) {
     // rows of an A tile that a copy brings: no more than there are
     const int box_a = p.a_t || p.m >= kTile ? kTile : int((p.m + 7) / 8 * 8);
     p.a_bytes = box_a * kTile;
@@ -540,14 +574,16 @@ cudaError_t launch_split(MatmulArgs p, const uint8_t* a, int64_t lda, const uint
     cudaError_t e = encode_codes(&map_a, a, p.m, p.k, lda, p.a_t, box_a);
     if (e == cudaSuccess) e = encode_codes(&map_b, b, p.n, p.k, ldb, p.b_t, kTile);
     if (e != cudaSuccess) return e;
-    p.stages = kSplitStageBytes / (p.a_bytes + kTileBytes + 2 * kScaleBytes);
-    const int64_t tiles = p.tiles_m * p.tiles_n, blocks = (p.k + kTile - 1) / kTile;
-    const int split = split_of(tiles, blocks);
-    const unsigned bytes = SplitSmem(p.stages, p.a_bytes).bytes(p.stages) + 1024;
-    e = cudaFuncSetAttribute(split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    const int64_t es = p.bf16 ? 2 : 4;
+    p.vec = SPLIT ? aligned(p.out, 4 * es) && p.ldo % 4 == 0 : aligned(p.out, 32) && p.ldo * es % 32 == 0;
+    p.stages = (kStageBytes - 4 * 32 * 33 * 4) / (p.a_bytes + kTileBytes + 2 * kScaleBytes);
+    const unsigned bytes = TileSmem(p.stages, p.a_bytes).bytes(p.stages) + 1024;
+    auto* kernel = p.bf16 ? tile_kernel<SPLIT, true> : tile_kernel<SPLIT, false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
+    const int64_t tiles = p.tiles_m * p.tiles_n;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(tiles * split));
+    cfg.gridDim = dim3(unsigned(SPLIT ? tiles * split : tiles < kSms ? tiles : kSms));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
@@ -556,8 +592,15 @@ cudaError_t launch_split(MatmulArgs p, const uint8_t* a, int64_t lda, const uint
     attr[0].val.clusterDim.x = split;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, split_kernel, map_a, map_b, p, split);
+    cfg.numAttrs = SPLIT ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, p, split);
+}
+
+cudaError_t launch(const MatmulArgs& p, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, cudaStream_t st) {
+    const int64_t blocks = (p.k + kTile - 1) / kTile;
+    if (p.m > kTile) return launch_pair(p, a, lda, b, ldb, st);
+    const int split = split_of(p.tiles_m * p.tiles_n, blocks);
+    return split > 1 ? launch_tiles<true>(p, a, lda, b, ldb, split, st) : launch_tiles<false>(p, a, lda, b, ldb, 1, st);
 }
 
 }  // namespace
@@ -612,7 +655,6 @@ extern "C" tsenor_status tsenor_matmul(tsenor_form form, const uint8_t* a, int64
     p.a_t = a_t;
     p.b_t = b_t;
     p.bf16 = dtype == TSENOR_BF16;
-    p.vec = aligned(out, 4 * es) && ldo % 4 == 0;
-    const cudaError_t e = m > kTile ? launch_pair(p, a, lda, b, ldb, st) : launch_split(p, a, lda, b, ldb, st);
+    const cudaError_t e = launch(p, a, lda, b, ldb, st);
     return e == cudaSuccess ? TSENOR_OK : cuda_fail(e, "tsenor_matmul launch");
 }
