@@ -377,8 +377,8 @@ tsenor_status tsenor_matmul(tsenor_form form, const uint8_t* a, int64_t lda, con
  * tsenor_distill_grad:  the gradient from lse, which the same logits gave.
  * grad has the type of the logits, ldg elements from row to row; it may be
  * the logits' own memory (same pointer, ldg == ld).  The sums are fp32 in a
- * fixed order: the same call gives the same bits.  TSENOR_ERR_SHAPE for top
- * or vocab above the limits.
+ * fixed order: the same call gives the same bits.  TSENOR_ERR_SHAPE for top,
+ * vocab or rows (2^24) above the limits.
  */
 #define TSENOR_DISTILL_MAX_TOP 1024
 #define TSENOR_DISTILL_MAX_VOCAB 262144

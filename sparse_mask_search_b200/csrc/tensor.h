@@ -1,0 +1,175 @@
+// Fifth-generation tensor core instructions (tcgen05) and what feeds them:
+// block-scaled 8-bit products (kind::mxf8f6f4), tensor memory, bulk copies and
+// cluster addresses.  GROUP is the number of CTAs that work on one tile (1, 2).
+#pragma once
+
+#include <cstdint>
+
+#include "tma.cuh"
+
+namespace tsenor {
+
+// ---- instruction and operand descriptors --------------------------------------------
+
+// kind::mxf8f6f4 with e4m3 operands, fp32 accumulator and one exponent byte
+// (ue8m0) per row and 32 of the contracted axis; bits 4-5 and 29-30 choose which
+// of the four bytes of a scale word an instruction uses.  t: the operand is
+// stored with its contracted axis along rows ("MN-major").
+__host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool a_t, bool b_t) {
+    return (uint32_t(a_t) << 15) | (uint32_t(b_t) << 16) | (uint32_t(n / 8) << 17) | (1u << 23) |
+           (uint32_t(m / 128) << 27);
+}
+__device__ __forceinline__ uint32_t with_scale_byte(uint32_t desc, uint32_t id) { return desc | (id << 4) | (id << 29); }
+
+// Operand tile in shared memory: 128-byte rows in the 128-byte swizzle that TMA
+// writes, 8 rows to a 1024-byte group.  sbo: bytes between groups of 8 rows;
+// lbo: bytes between 128-byte wide column groups (MN-major tiles wider than 128).
+__device__ __forceinline__ uint64_t tile_desc(uint32_t smem, uint32_t lbo) {
+    return uint64_t((smem >> 4) & 0x3fffu) | (uint64_t(lbo >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// Scale entry of 32 rows of 16 bytes, not swizzled, 8 rows to a 128-byte group.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem) {
+    return uint64_t((smem >> 4) & 0x3fffu) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+}
+
+// ---- tensor memory ------------------------------------------------------------------
+
+template <int GROUP>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, int cols) {     // one warp, cols a power of two >= 32
+    if constexpr (GROUP == 1)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(slot)), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(slot)), "r"(cols) : "memory");
+}
+template <int GROUP>
+__device__ __forceinline__ void tmem_free(uint32_t tmem, int cols) {       // the warp that allocated
+    if constexpr (GROUP == 1) {
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+    } else {
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+    }
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 lanes (the warp's quarter of the 128) x 32 columns, one row to a thread.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ---- asynchronous tensor core work (one thread; runs in issue order) ------------------
+
+// True in one lane of a converged warp.  The roles below keep the whole warp in their
+// loops and elect a lane around the instructions themselves: descriptors and
+// addresses are then known to be the same in all lanes and sit in uniform
+// registers.  Loops entered by one lane alone cost 86 cycles for each mma that was issued.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
+// One scale entry (512 bytes) to 4 columns of tensor memory, repeated in each quarter of the lanes.
+template <int GROUP>
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+    if constexpr (GROUP == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// D (+)= A B over 32 of the contracted axis, each side times its scales.
+template <int GROUP>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                           bool add) {
+    if constexpr (GROUP == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(add)) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(add)) : "memory");
+}
+
+// Arrives on `bar` when this thread's earlier tensor core work is done.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 ::"r"(smem_u32(bar)) : "memory");
+}
+// The same on the barrier at this place in both CTAs of the pair.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
+}
+
+// ---- copies and clusters ----------------------------------------------------------------
+
+// `bytes` (a multiple of 16, both ends 16-byte aligned) from global memory into this CTA.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(dst)), "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// Tile load into this CTA that completes on a barrier of either CTA of the pair
+// (`bar`: its address in the cluster).
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Arrival on a barrier of any CTA of the cluster.
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// 32 bytes to a 32-byte aligned address in one store.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+}
+
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of this CTA's shared address `smem` in the CTA of rank `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t smem, unsigned rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+}  // namespace tsenor
