@@ -41,6 +41,7 @@ struct DistillArgs {
     int top;
     const float* teacher_lse;
     float temperature;
+    double inv_t;                                // 1 / temperature
     const float* weight;
     float* loss;
     float* lse;
@@ -82,27 +83,6 @@ __device__ __forceinline__ void set_pair(uint32_t (&w)[4], int i, float2 x) {
     }
 }
 
-struct Max {
-    __device__ static float of(float a, float b) { return fmaxf(a, b); }
-};
-struct Sum {
-    template <typename X>
-    __device__ static X of(X a, X b) { return a + b; }
-};
-// Over the block, in a fixed order; the result in every thread.
-template <typename Op, typename X>
-__device__ X reduce(X v, X* red) {
-#pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) v = Op::of(v, __shfl_xor_sync(kFullMask, v, s));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int k = 1; k < kWarps; ++k) v = Op::of(v, red[k]);
-    __syncthreads();
-    return v;
-}
-
 // A row's columns in memory: `head` entries up to the first 16-byte boundary, `chunks` of 16
 // bytes, `tail` entries.  Slice r of n has a share of the chunks; the first also
 // has the head, the last the tail.
@@ -116,9 +96,9 @@ struct Slice {
     __device__ Slice(const typename T::storage* z, int vocab_, int r, int n) : vocab(vocab_) {
         int h = int(((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / sizeof(typename T::storage));
         if (h > vocab) h = vocab;
-        const int all = (vocab - h) / kPer;
-        chunk0 = int(int64_t(all) * r / n);
-        chunks = int(int64_t(all) * (r + 1) / n) - chunk0;
+        const int all = (vocab - h) / kPer, share = int(unsigned(all + n - 1) / unsigned(n));
+        chunk0 = r * share < all ? r * share : all;
+        chunks = all - chunk0 < share ? all - chunk0 : share;
         head = r == 0 ? h : 0;
         tail = r == n - 1 ? vocab - h - all * kPer : 0;
         first = h + chunk0 * kPer;
@@ -132,70 +112,113 @@ struct Slice {
 
 // The teacher's entries of a row in shared memory, their number rounded up to 4.
 struct Teacher {
+    int top, top4, slots;
+    float* logp;                                 // t_j / T until weights() has run
     float* p;
     int* index;                                  // 16-byte aligned; -1: no entry
-    float* target;                               // grad_kernel: the gradient of the entry's column
+    int* table;                                  // of the indices seen, open addressing; `slots` a power of two
 
-    __device__ Teacher(void* at, int top) : p(static_cast<float*>(at)) {
-        index = reinterpret_cast<int*>(p + (top + 3) / 4 * 4);
-        target = reinterpret_cast<float*>(index + (top + 3) / 4 * 4);
+    __host__ __device__ static int slots_of(int top) {
+        int n = 32;
+        while (n < 2 * top) n *= 2;
+        return n;
     }
-};
+    __host__ static unsigned bytes(int top) { return unsigned((top + 3) / 4 * 4 * 12 + slots_of(top) * 4); }
+    __device__ Teacher(void* at, int top_) : top(top_), top4((top_ + 3) / 4 * 4), slots(slots_of(top_)) {
+        logp = static_cast<float*>(at);
+        p = logp + top4;
+        index = reinterpret_cast<int*>(p + top4);
+        table = index + top4;
+    }
 
-// Fills idx and p; returns P = sum p.  `empty`: no entry has weight; `bad`: the row fails.
-__device__ float teacher_weights(const DistillArgs& a, int64_t row, const Teacher& s, float* red, bool* empty, bool* bad) {
-    bool wrong = false;
-    float high = -INFINITY;
-    for (int j = threadIdx.x; j < (a.top + 3) / 4 * 4; j += kThreads) {
-        const int i = j < a.top ? a.index[row * a.top + j] : -1;
-        const float v = j < a.top ? a.top_logits[row * a.top + j] / a.temperature : 0.f;
-        wrong = wrong || i >= a.vocab || (i >= 0 && !(v < INFINITY));
-        const bool in = i >= 0 && i < a.vocab;
-        s.index[j] = in ? i : -1;
-        s.p[j] = in ? v : -INFINITY;
-        high = fmaxf(high, s.p[j]);
+    // All threads.  Reads the entries; empty: none has weight, bad: the row fails.
+    __device__ void read_entries(const DistillArgs& a, int64_t row, bool* empty, bool* bad) {
+        for (int i = threadIdx.x; i < slots; i += kThreads) table[i] = -1;
+        bool wrong = a.teacher_lse && !(fabsf(a.teacher_lse[row]) < INFINITY), any = false;
+        for (int j = threadIdx.x; j < top4; j += kThreads) {
+            const int i = j < top ? a.index[row * top + j] : -1;
+            const float v = j < top ? a.top_logits[row * top + j] / a.temperature : 0.f;
+            const bool in = i >= 0 && i < a.vocab;
+            wrong = wrong || (i >= 0 && !(in && v < INFINITY));
+            any = any || (in && v > -INFINITY) || i >= a.vocab || (i >= 0 && v != v);
+            index[j] = in ? i : -1;
+            logp[j] = in ? v : -INFINITY;
+        }
+        *empty = !__syncthreads_or(any);
+        *bad = __syncthreads_or(wrong) && !*empty;
     }
-    high = reduce<Max>(high, red);
-    *empty = high == -INFINITY;
-    float c = 0.f;
-    if (!*empty) {
+    // All threads, after read_entries and before a barrier: marks the indices that more than one entry has.
+    __device__ void mark_twins() const {
+        for (int j = threadIdx.x; j < top; j += kThreads) {
+            const int v = index[j];
+            if (v < 0) continue;
+            for (unsigned h = first_slot(v);; ++h) {                         // half of the slots stay free
+                int* slot = table + (h & (slots - 1));
+                const int was = atomicCAS(slot, -1, v);
+                if (was == -1) break;
+                if ((was & ~kTwin) == v) {
+                    atomicOr(slot, kTwin);
+                    break;
+                }
+            }
+        }
+    }
+    __device__ bool has_twin(int v) const {
+        unsigned h = first_slot(v);
+        while ((table[h & (slots - 1)] & ~kTwin) != v) ++h;
+        return table[h & (slots - 1)] & kTwin;
+    }
+    static constexpr int kTwin = 1 << 30;        // above every column
+    __device__ static unsigned first_slot(int v) { return (unsigned(v) * 2654435761u) >> 7; }
+    // One warp, after read_entries: log p and p; P = sum p.
+    __device__ float weights(const DistillArgs& a, int64_t row) const {
+        const int lane = threadIdx.x & 31;
+        float c;
         if (a.teacher_lse) {
             c = a.teacher_lse[row];
-            wrong = wrong || !(fabsf(c) < INFINITY);
         } else {
-            float sum = 0.f;
-            for (int j = threadIdx.x; j < a.top; j += kThreads) sum += expf(s.p[j] - high);
-            c = high + logf(reduce<Sum>(sum, red));
+            float high = -INFINITY, sum = 0.f;
+            for (int j = lane; j < top; j += 32) high = fmaxf(high, logp[j]);
+#pragma unroll
+            for (int s = 16; s >= 1; s >>= 1) high = fmaxf(high, __shfl_xor_sync(kFullMask, high, s));
+            for (int j = lane; j < top; j += 32) sum += expf(logp[j] - high);
+#pragma unroll
+            for (int s = 16; s >= 1; s >>= 1) sum += __shfl_xor_sync(kFullMask, sum, s);
+            c = high + logf(sum);
+        }
+        float total = 0.f;
+        for (int j = lane; j < top4; j += 32) {
+            const float l = logp[j] - c, w = expf(l);
+            logp[j] = l;
+            p[j] = w;
+            total += w;
+        }
+#pragma unroll
+        for (int s = 16; s >= 1; s >>= 1) total += __shfl_xor_sync(kFullMask, total, s);
+        return total;
+    }
+    // All threads: f(j, v, sum of the weights of index v) for the entries in a slice, each index once.
+    template <typename S, typename F>
+    __device__ __forceinline__ void each(const S& slice, F f) const {
+        for (int j = threadIdx.x; j < top; j += kThreads) {
+            const int v = index[j];
+            if (v < 0 || !slice.has(v)) continue;
+            bool first = true;
+            float w = p[j];
+            if (has_twin(v)) {                   // in the order of the entries
+                w = 0.f;
+                for (int k = 0; k < top4; k += 4) {
+                    const int4 o = *reinterpret_cast<const int4*>(index + k);
+                    if (o.x == v) { first = first && k >= j; w += p[k]; }
+                    if (o.y == v) { first = first && k + 1 >= j; w += p[k + 1]; }
+                    if (o.z == v) { first = first && k + 2 >= j; w += p[k + 2]; }
+                    if (o.w == v) { first = first && k + 3 >= j; w += p[k + 3]; }
+                }
+            }
+            if (first) f(j, v, w);
         }
     }
-    float total = 0.f;
-    for (int j = threadIdx.x; j < a.top; j += kThreads) {
-        const float w = *empty ? 0.f : expf(s.p[j] - c);
-        s.p[j] = w;
-        total += w;
-    }
-    *bad = __syncthreads_or(wrong);
-    return reduce<Sum>(total, red);
-}
-
-// Calls f(j, v, sum of the weights of index v) for the entries of a slice, each index once.
-template <typename T, typename F>
-__device__ __forceinline__ void each_target(const Teacher& s, int top, const Slice<T>& slice, F f) {
-    for (int j = threadIdx.x; j < top; j += kThreads) {
-        const int v = s.index[j];
-        if (v < 0 || !slice.has(v)) continue;
-        bool first = true;
-        float w = 0.f;
-        for (int k = 0; k < top; k += 4) {
-            const int4 o = *reinterpret_cast<const int4*>(s.index + k);
-            if (o.x == v) { first = first && k >= j; w += s.p[k]; }
-            if (o.y == v) { first = first && k + 1 >= j; w += s.p[k + 1]; }
-            if (o.z == v) { first = first && k + 2 >= j; w += s.p[k + 2]; }
-            if (o.w == v) { first = first && k + 3 >= j; w += s.p[k + 3]; }
-        }
-        if (first) f(j, v, w);
-    }
-}
+};
 
 // Gradient 0 for the columns of a slice.
 template <typename T>
@@ -226,9 +249,33 @@ __device__ __forceinline__ void write_chunk(typename T::storage* g, const uint4&
     }
 }
 
+// A softmax normaliser in units of z: sum of 2^((z - high) scale).  A part without a
+// finite logit has high -inf and sum 0, or NaN if it holds one; both survive the joins.
+struct Norm {
+    float high, sum;
+};
+__device__ __forceinline__ float finite_base(float high) { return high == -INFINITY ? 0.f : high; }
+// `n` normalisers, read through get(k).
+template <typename F>
+__device__ __forceinline__ Norm join(int n, float scale2, F get) {
+    Norm all{-INFINITY, 0.f};
+    for (int k = 0; k < n; ++k) all.high = fmaxf(all.high, get(k).high);
+    const float base = finite_base(all.high);
+    for (int k = 0; k < n; ++k) {
+        const Norm o = get(k);
+        all.sum += o.sum * ex2((o.high - base) * scale2);
+    }
+    return all;
+}
+// log of a sum of 1 or more in fp64: the exponent apart, so that logf sees [1, 2).
+__device__ __forceinline__ double log_sum(float s) {
+    const int e = int(__float_as_uint(s) >> 23) - 127;
+    return double(e) * 0.6931471805599453 + double(logf(__uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u)));
+}
+
 // What a slice tells the others of its row.
 struct Share {
-    float high, sum;
+    Norm norm;
     double term;
 };
 
@@ -236,35 +283,38 @@ struct Share {
 template <typename T, bool STEP>
 __global__ void __launch_bounds__(kThreads) loss_kernel(const DistillArgs a, const int slices, const int chunk_room) {
     extern __shared__ __align__(128) uint4 chunk[];
-    __shared__ float red[kWarps];
-    __shared__ double red64[kWarps];
-    __shared__ Share share[kMaxSlices];
+    __shared__ Share share[kMaxSlices], part[kWarps];
     __shared__ float extra[2 * Slice<T>::kPer];
-    __shared__ float row_high, row_sum;
+    __shared__ float total_of_p;
     __shared__ uint64_t bar[kSegments];
-    const int t = threadIdx.x;
+    constexpr int kPer = Slice<T>::kPer;
+    constexpr int kGroup = 4;                    // chunks that share a step of the running maximum
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int64_t row = blockIdx.x / slices;
     const int rank = slices > 1 ? int(cluster_rank()) : 0;
     const auto* z = static_cast<const typename T::storage*>(a.logits) + row * a.ld;
     auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
     const Slice<T> slice(z, int(a.vocab), rank, slices);
-    const Teacher teacher(chunk + chunk_room, a.top);
+    Teacher teacher(chunk + chunk_room, a.top);
     const bool vec = STEP && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     if (slices > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");      // every CTA of the row has begun
 
-    auto start_copy = [&] {                      // one thread; segment i has chunks [chunks i / kSegments, ...)
-        for (int i = 0; i < kSegments; ++i) mbar_init(bar + i, 1);
-        mbar_init_fence();
+    auto segment = [&](int i) { return slice.chunks * i / kSegments; };           // first chunk of segment i
+    auto start_copy = [&] {                      // one thread
         for (int i = 0; i < kSegments; ++i) {
-            const int c0 = slice.chunks * i / kSegments, n = slice.chunks * (i + 1) / kSegments - c0;
+            const int c = segment(i), n = segment(i + 1) - c;
             mbar_arrive_expect_tx(bar + i, n * 16);
-            if (n > 0) bulk_load(chunk + c0, z + slice.first + c0 * Slice<T>::kPer, n * 16, bar + i);
+            if (n > 0) bulk_load(chunk + c, z + slice.first + c * kPer, n * 16, bar + i);
         }
     };
-    if (!STEP && t == 0) start_copy();
+    if (t == 0) {
+        for (int i = 0; i < kSegments; ++i) mbar_init(bar + i, 1);
+        mbar_init_fence();
+        if (!STEP) start_copy();
+    }
     if (t < slice.extras()) extra[t] = read<T>(z + slice.extra(t));
     bool empty, bad;
-    const float total = teacher_weights(a, row, teacher, red, &empty, &bad);
+    teacher.read_entries(a, row, &empty, &bad);
     if (STEP && (empty || bad)) {                // the logits are not read
         if (slices > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         write_zeros<T>(g, slice, vec);
@@ -275,121 +325,142 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const DistillArgs a, con
         return;
     }
     if (STEP && t == 0) start_copy();
-    if (STEP) __syncthreads();
+    if (STEP) teacher.mark_twins();
+    if (warp == 0 && !empty) {                   // the others wait for the copy meanwhile
+        const float total = teacher.weights(a, row);
+        if (lane == 0) total_of_p = total;
+    }
 
+    // one pass over the slice; a NaN or +inf anywhere makes the sum NaN
     const float inv_t = 1.f / a.temperature, scale2 = inv_t * kLog2E;
-    float high = -INFINITY;
+    const float2 by2 = make_float2(scale2, scale2);
+    Norm norm{-INFINITY, 0.f};
     bool stalled = false;
     for (int i = 0; i < kSegments; ++i) {
         if (!mbar_wait_bounded(bar + i, 0)) stalled = true;
-        const int c1 = slice.chunks * (i + 1) / kSegments;
-        for (int c = slice.chunks * i / kSegments + t; c < c1; c += kThreads) {
-            const uint4 v = chunk[c];
-            if constexpr (std::is_same<T, BF16>::value) {
-                uint32_t m, n;
-                asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(v.x), "r"(v.y));
-                asm("max.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(v.z), "r"(v.w));
-                asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
-                high = fmaxf(high, fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u)));
-            } else {
-                high = fmaxf(high, fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
-                                         fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))));
-            }
-        }
-    }
-    if (t < slice.extras()) high = fmaxf(high, extra[t]);
-    high = reduce<Max>(high, red);
-    // a NaN or +inf anywhere makes the sum NaN
-    const float base = high == -INFINITY ? 0.f : high;
-    const float2 minus = make_float2(-base, -base), by2 = make_float2(scale2, scale2);
-    float2 sum2 = make_float2(0.f, 0.f);
-    for (int c = t; c < slice.chunks; c += kThreads) {
-        const uint4 v = chunk[c];
+        const int end = segment(i + 1);
+        for (int c = segment(i) + t; c < end; c += kGroup * kThreads) {
+            uint4 v[kGroup];
+            float high = norm.high;
 #pragma unroll
-        for (int i = 0; i < Slice<T>::kPer / 2; ++i) {
-            const float2 x = mul2(add2(pair_of<T>(v, i), minus), by2);
-            sum2 = add2(sum2, make_float2(ex2(x.x), ex2(x.y)));
+            for (int k = 0; k < kGroup; ++k) {
+                if (c + k * kThreads >= end) break;
+                v[k] = chunk[c + k * kThreads];
+                if constexpr (std::is_same<T, BF16>::value) {
+                    uint32_t m, n;
+                    asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(v[k].x), "r"(v[k].y));
+                    asm("max.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(v[k].z), "r"(v[k].w));
+                    asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
+                    high = fmaxf(high, fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u)));
+                } else {
+                    high = fmaxf(high, fmaxf(fmaxf(__uint_as_float(v[k].x), __uint_as_float(v[k].y)),
+                                             fmaxf(__uint_as_float(v[k].z), __uint_as_float(v[k].w))));
+                }
+            }
+            const float base = finite_base(high);
+            const float2 minus = make_float2(-base, -base);
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) {
+                if (c + k * kThreads >= end) break;
+#pragma unroll
+                for (int q = 0; q < kPer / 2; ++q) {
+                    const float2 x = mul2(add2(pair_of<T>(v[k], q), minus), by2);
+                    sum = add2(sum, make_float2(ex2(x.x), ex2(x.y)));
+                }
+            }
+            norm.sum = fmaf(norm.sum, ex2((norm.high - base) * scale2), sum.x + sum.y);
+            norm.high = high;
         }
     }
-    float sum = sum2.x + sum2.y;
-    if (t < slice.extras()) sum += ex2((extra[t] - base) * scale2);
-    if (stalled) sum = NAN;
-    sum = reduce<Sum>(sum, red);
+    if (t < slice.extras()) {
+        const float x = extra[t];
+        const Norm two[2] = {norm, Norm{x == x ? x : -INFINITY, x == x ? (x == -INFINITY ? 0.f : 1.f) : x}};
+        norm = join(2, scale2, [&](int k) { return two[k]; });
+    }
+    if (stalled) norm.sum = NAN;
+    float high = norm.high;
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) high = fmaxf(high, __shfl_xor_sync(kFullMask, high, s));
+    norm.sum *= ex2((norm.high - finite_base(high)) * scale2);
+    norm.high = high;
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) norm.sum += __shfl_xor_sync(kFullMask, norm.sum, s);
+    __syncthreads();
 
-    // sum_j p_j (log p_j - z_j / T) of the entries in this slice; their logits replace nothing yet
+    // sum_j p_j (log p_j - z_j / T) of the entries in this slice
     auto logit_at = [&](int v) {
         if (v < slice.head) return extra[v];
-        if (v >= slice.first && v < slice.first + slice.chunks * Slice<T>::kPer)
+        if (v >= slice.first && v < slice.first + slice.chunks * kPer)
             return read<T>(reinterpret_cast<const typename T::storage*>(chunk) + (v - slice.first));
         return extra[slice.head + v - (slice.vocab - slice.tail)];
     };
     double term = 0.0;
-    for (int j = t; j < a.top; j += kThreads) {
-        const int v = teacher.index[j];
-        const float w = teacher.p[j];
-        if (v >= 0 && w > 0.f && slice.has(v))
-            term += double(w) * (log(double(w)) - double(logit_at(v)) / double(a.temperature));
-    }
-    term = reduce<Sum>(term, red64);
+    if (!empty)
+        for (int j = t; j < a.top; j += kThreads) {
+            const int v = teacher.index[j];
+            const float w = teacher.p[j];
+            if (v >= 0 && w > 0.f && slice.has(v))
+                term += double(w) * (double(teacher.logp[j]) - double(logit_at(v)) * a.inv_t);
+        }
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) term += __shfl_xor_sync(kFullMask, term, s);
+    if (lane == 0) part[warp] = Share{norm, term};
+    __syncthreads();
+    auto sum_terms = [](const Share* s, int n) {
+        double x = s[0].term;
+        for (int k = 1; k < n; ++k) x += s[k].term;
+        return x;
+    };
+    norm = join(kWarps, scale2, [&](int k) { return part[k].norm; });
     if (slices > 1) {
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         if (t < slices) {
             const uint32_t to = cluster_addr(smem_u32(share + rank), t);
-            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(high), "f"(sum) : "memory");
-            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to + 8), "d"(term) : "memory");
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(norm.high), "f"(norm.sum) : "memory");
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to + 8), "d"(sum_terms(part, kWarps)) : "memory");
         }
         cluster_sync();
-    } else if (t == 0) {
-        share[0] = Share{high, sum, term};
+        norm = join(slices, scale2, [&](int k) { return share[k].norm; });
     }
-    if (t == 0) {
-        float m = share[0].high;
-        for (int k = 1; k < slices; ++k) m = fmaxf(m, share[k].high);
-        float s = 0.f;
-        double all = 0.0;
-        for (int k = 0; k < slices; ++k) {
-            // a slice without a finite logit adds nothing, but a NaN
-            s += share[k].high == -INFINITY ? share[k].sum : share[k].sum * ex2((share[k].high - m) * scale2);
-            all += share[k].term;
-        }
-        const double lse = m == -INFINITY ? double(m) : double(m) / double(a.temperature) + log(double(s));
-        const bool failed = bad || (!empty && !(fabs(lse) < double(INFINITY)));
-        if (rank == 0) {
-            a.loss[row] = failed ? NAN : empty ? 0.f
-                          : float(double(a.temperature) * double(a.temperature) * (all + double(total) * lse));
-            if (!STEP) a.lse[row] = failed ? NAN : float(lse);
-            if (failed) atomicAdd(&g_row_failures, 1ull);
-        }
-        row_high = m;
-        row_sum = failed ? 0.f : s;
+    const float m = norm.high;
+    const bool failed = bad || (!empty && !(fabsf(m) < INFINITY && norm.sum < INFINITY));
+    if (t == 0 && rank == 0) {
+        const double lse = m == -INFINITY ? double(m + norm.sum)              // no finite logit: -inf, or NaN
+                                          : double(m) * a.inv_t + log_sum(norm.sum);
+        const double all = slices > 1 ? sum_terms(share, slices) : sum_terms(part, kWarps);
+        a.loss[row] = failed ? NAN : empty ? 0.f
+                      : float(double(a.temperature) * double(a.temperature) * (all + double(total_of_p) * lse));
+        if (!STEP) a.lse[row] = failed ? NAN : float(lse);
+        if (failed) atomicAdd(&g_row_failures, 1ull);
     }
     if constexpr (STEP) {
-        __syncthreads();
         const float by = a.temperature * (a.weight ? a.weight[row] : 1.f);
-        if (row_sum == 0.f || by == 0.f) {
+        if (failed || by == 0.f) {
             write_zeros<T>(g, slice, vec);
             return;
         }
-        const float scale = by * total / row_sum, m = row_high;
+        const float scale = by * total_of_p / norm.sum;
         auto at = [&](float x) { return scale * ex2((x - m) * scale2); };
         const float2 minus_m = make_float2(-m, -m), scale_2 = make_float2(scale, scale);
+#pragma unroll 4
         for (int c = t; c < slice.chunks; c += kThreads)
-            write_chunk<T>(g + slice.first + c * Slice<T>::kPer, chunk[c], vec, [&](float2 x) {
+            write_chunk<T>(g + slice.first + c * kPer, chunk[c], vec, [&](float2 x) {
                 x = mul2(add2(x, minus_m), by2);
                 return mul2(make_float2(ex2(x.x), ex2(x.y)), scale_2);
             });
         if (t < slice.extras()) write<T>(g + slice.extra(t), at(extra[t]));
         __syncthreads();                         // the entries' columns are written again
-        each_target<T>(teacher, a.top, slice, [&](int, int v, float w) { write<T>(g + v, at(logit_at(v)) - by * w); });
+        teacher.each(slice, [&](int, int v, float w) { write<T>(g + v, at(logit_at(v)) - by * w); });
     }
 }
 
 // The gradient from lse; blockIdx.x is a row's slice.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, const int slices) {
-    extern __shared__ __align__(128) uint4 chunk[];
-    __shared__ float red[kWarps];
-    const Teacher teacher(chunk, a.top);
+    extern __shared__ __align__(128) uint4 room[];
+    __shared__ float total_of_p;
+    constexpr int kPer = Slice<T>::kPer;
     constexpr int kAhead = 4;                    // chunks of a thread in flight
     const int t = threadIdx.x;
     const int64_t row = blockIdx.x / slices;
@@ -397,9 +468,11 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     const auto* z = static_cast<const typename T::storage*>(a.logits) + row * a.ld;
     auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
     const Slice<T> slice(z, int(a.vocab), rank, slices);
+    Teacher teacher(room, a.top);
+    float* target = teacher.logp;                // log p is not needed here
     const bool vec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     bool empty, bad;
-    const float total = teacher_weights(a, row, teacher, red, &empty, &bad);
+    teacher.read_entries(a, row, &empty, &bad);
     const float lse = a.lse[row];
     const float by = a.temperature * (a.weight ? a.weight[row] : 1.f);
     bad = bad || (!empty && !(fabsf(lse) < INFINITY));
@@ -408,30 +481,40 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
         write_zeros<T>(g, slice, vec);
         return;
     }
-    const float inv_t = 1.f / a.temperature, scale = by * total;
-    auto at = [&](float x) { return scale * ex2(fmaf(x, inv_t, -lse) * kLog2E); };
-    // the entries' gradients before anything is written: grad may be the logits
-    each_target<T>(teacher, a.top, slice, [&](int j, int v, float w) { teacher.target[j] = at(read<T>(z + v)) - by * w; });
-    __syncthreads();
     const uint4* in = reinterpret_cast<const uint4*>(z + slice.first);
-    const float2 inv2 = make_float2(inv_t, inv_t), minus = make_float2(-lse, -lse), l2 = make_float2(kLog2E, kLog2E),
-                 scale_2 = make_float2(scale, scale);
-    for (int c = t; c < slice.chunks; c += kAhead * kThreads) {
-        uint4 v[kAhead];
+    uint4 v[kAhead];
+    auto load = [&](int c) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             if (c + i * kThreads < slice.chunks) v[i] = in[c + i * kThreads];
+    };
+    load(t);                                     // on their way while the weights are made
+    teacher.mark_twins();
+    if (t < 32) {
+        const float total = teacher.weights(a, row);
+        if (t == 0) total_of_p = total;
+    }
+    __syncthreads();
+    const float inv_t = 1.f / a.temperature, scale = by * total_of_p;
+    auto at = [&](float x) { return scale * ex2(fmaf(x, inv_t, -lse) * kLog2E); };
+    // the entries' gradients before anything is written: grad may be the logits
+    teacher.each(slice, [&](int j, int c, float w) { target[j] = at(read<T>(z + c)) - by * w; });
+    __syncthreads();
+    const float2 inv2 = make_float2(inv_t, inv_t), minus = make_float2(-lse, -lse), l2 = make_float2(kLog2E, kLog2E),
+                 scale_2 = make_float2(scale, scale);
+    for (int c = t; c < slice.chunks; c += kAhead * kThreads) {
+        if (c != t) load(c);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             if (c + i * kThreads < slice.chunks)
-                write_chunk<T>(g + slice.first + (c + i * kThreads) * Slice<T>::kPer, v[i], vec, [&](float2 x) {
+                write_chunk<T>(g + slice.first + (c + i * kThreads) * kPer, v[i], vec, [&](float2 x) {
                     x = mul2(fma2(x, inv2, minus), l2);
                     return mul2(make_float2(ex2(x.x), ex2(x.y)), scale_2);
                 });
     }
     if (t < slice.extras()) write<T>(g + slice.extra(t), at(read<T>(z + slice.extra(t))));
     __syncthreads();
-    each_target<T>(teacher, a.top, slice, [&](int j, int v, float) { write<T>(g + v, teacher.target[j]); });
+    teacher.each(slice, [&](int j, int c, float) { write<T>(g + c, target[j]); });
 }
 
 // Slices of a row: at most kSliceBytes each, and for few rows enough CTAs to fill the
@@ -447,7 +530,7 @@ cudaError_t launch_loss(const DistillArgs& a, cudaStream_t st) {
     const int64_t row_bytes = a.vocab * int64_t(sizeof(typename T::storage));
     const int slices = slices_of(a.rows, row_bytes);
     const int chunk_room = int((row_bytes / 16 + slices - 1) / slices);
-    const unsigned bytes = unsigned(chunk_room * 16 + (a.top + 3) / 4 * 4 * 8);
+    const unsigned bytes = unsigned(chunk_room * 16) + Teacher::bytes(a.top);
     cudaError_t e = cudaFuncSetAttribute(loss_kernel<T, STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -470,7 +553,7 @@ cudaError_t launch_grad(const DistillArgs& a, cudaStream_t st) {
     const int64_t row_bytes = a.vocab * int64_t(sizeof(typename T::storage));
     const int slices = a.rows >= 296 ? int((row_bytes + kSliceBytes - 1) / kSliceBytes)
                                      : int((row_bytes + kSliceBytes / 8 - 1) / (kSliceBytes / 8));
-    grad_kernel<T><<<unsigned(a.rows * slices), kThreads, (a.top + 3) / 4 * 4 * 12, st>>>(a, slices);
+    grad_kernel<T><<<unsigned(a.rows * slices), kThreads, Teacher::bytes(a.top), st>>>(a, slices);
     return cudaGetLastError();
 }
 
@@ -518,7 +601,8 @@ extern "C" tsenor_status tsenor_distill_loss(const void* logits, tsenor_dtype dt
                                              int64_t ld, const int32_t* index, const float* top_logits, int top,
                                              const float* teacher_lse, float temperature, float* loss, float* lse,
                                              tsenor_stream_t stream) {
-    const DistillArgs a{logits, rows, vocab, ld, index, top_logits, top, teacher_lse, temperature, nullptr, loss, lse,
+    const DistillArgs a{logits, rows, vocab, ld, index, top_logits, top, teacher_lse, temperature, 1.0 / temperature,
+                        nullptr, loss, lse,
                         nullptr, 0};
     const tsenor_status s = check_distill(dtype, a);
     if (s != TSENOR_OK || rows == 0) return s;
@@ -532,8 +616,8 @@ extern "C" tsenor_status tsenor_distill_step(const void* logits, tsenor_dtype dt
                                              int64_t ld, const int32_t* index, const float* top_logits, int top,
                                              const float* teacher_lse, float temperature, const float* weight,
                                              float* loss, void* grad, int64_t ldg, tsenor_stream_t stream) {
-    const DistillArgs a{logits, rows, vocab, ld, index, top_logits, top, teacher_lse, temperature, weight, loss,
-                        nullptr, grad, ldg};
+    const DistillArgs a{logits, rows, vocab, ld, index, top_logits, top, teacher_lse, temperature, 1.0 / temperature,
+                        weight, loss, nullptr, grad, ldg};
     const tsenor_status s = check_distill(dtype, a);
     if (s != TSENOR_OK || rows == 0) return s;
     if (!loss || !aligned(loss, 4) || !grad_ok(dtype, a)) return TSENOR_ERR_ARG;
@@ -546,8 +630,8 @@ extern "C" tsenor_status tsenor_distill_grad(const void* logits, tsenor_dtype dt
                                              int64_t ld, const int32_t* index, const float* top_logits, int top,
                                              const float* teacher_lse, float temperature, const float* lse,
                                              const float* weight, void* grad, int64_t ldg, tsenor_stream_t stream) {
-    const DistillArgs a{logits, rows, vocab, ld, index, top_logits, top, teacher_lse, temperature, weight, nullptr,
-                        const_cast<float*>(lse), grad, ldg};
+    const DistillArgs a{logits, rows, vocab, ld, index, top_logits, top, teacher_lse, temperature, 1.0 / temperature,
+                        weight, nullptr, const_cast<float*>(lse), grad, ldg};
     const tsenor_status s = check_distill(dtype, a);
     if (s != TSENOR_OK || rows == 0) return s;
     if (!lse || !aligned(lse, 4) || !grad_ok(dtype, a)) return TSENOR_ERR_ARG;
