@@ -27,8 +27,11 @@ __device__ unsigned long long g_row_failures;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kTeachers = 128;                   // further threads of loss_kernel
 constexpr int kMaxTop = TSENOR_DISTILL_MAX_TOP;
-constexpr int kSegments = 4;                     // of a slice's copy, each with its own barrier
+constexpr int kGroup = 4;                        // chunks of a thread that share a step of the running maximum
+constexpr int kSegment = kGroup * kThreads;      // chunks of a slice that are copied under one barrier
+constexpr int kMaxSegments = 8;                  // of the largest slice, 128 KB
 constexpr int kMaxSlices = 8;
 constexpr int kSliceBytes = 64 * 1024;
 constexpr float kLog2E = 1.4426950408889634f;
@@ -110,7 +113,40 @@ struct Slice {
     }
 };
 
+// N threads of a block, from thread FIRST on, that meet at the block's barrier 1.
+template <int FIRST, int N>
+struct Team {
+    __device__ static int id() { return int(threadIdx.x) - FIRST; }
+    __device__ static void sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
+    __device__ static bool any(bool x) {
+        uint32_t r;
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\tbar.red.or.pred p, 1, %2, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+                     : "=r"(r) : "r"(uint32_t(x)), "n"(N) : "memory");
+        return r != 0;
+    }
+    // In a fixed order; the result in every thread.  `red`: N / 32 values that may be used again after the next call.
+    template <typename X, typename F>
+    __device__ static X reduce(X v, X* red, F f) {
+#pragma unroll
+        for (int s = 16; s >= 1; s >>= 1) v = f(v, __shfl_xor_sync(kFullMask, v, s));
+        if ((threadIdx.x & 31) == 0) red[id() / 32] = v;
+        sync();
+        v = red[0];
+#pragma unroll
+        for (int k = 1; k < N / 32; ++k) v = f(v, red[k]);
+        return v;
+    }
+};
+struct Larger {
+    __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct Plus {
+    __device__ float operator()(float a, float b) const { return a + b; }
+    __device__ double operator()(double a, double b) const { return a + b; }
+};
+
 // The teacher's entries of a row in shared memory, their number rounded up to 4.
+template <typename TEAM, int N>
 struct Teacher {
     int top, top4, slots;
     float* logp;                                 // t_j / T until weights() has run
@@ -118,24 +154,18 @@ struct Teacher {
     int* index;                                  // 16-byte aligned; -1: no entry
     int* table;                                  // of the indices seen, open addressing; `slots` a power of two
 
-    __host__ __device__ static int slots_of(int top) {
-        int n = 32;
-        while (n < 2 * top) n *= 2;
-        return n;
-    }
-    __host__ static unsigned bytes(int top) { return unsigned((top + 3) / 4 * 4 * 12 + slots_of(top) * 4); }
-    __device__ Teacher(void* at, int top_) : top(top_), top4((top_ + 3) / 4 * 4), slots(slots_of(top_)) {
+    __device__ Teacher(void* at, int top_, int slots_) : top(top_), top4((top_ + 3) / 4 * 4), slots(slots_) {
         logp = static_cast<float*>(at);
         p = logp + top4;
         index = reinterpret_cast<int*>(p + top4);
         table = index + top4;
     }
 
-    // All threads.  Reads the entries; empty: none has weight, bad: the row fails.
+    // Reads the entries; empty: none has weight, bad: the row fails.
     __device__ void read_entries(const DistillArgs& a, int64_t row, bool* empty, bool* bad) {
-        for (int i = threadIdx.x; i < slots; i += kThreads) table[i] = -1;
+        for (int i = TEAM::id(); i < slots; i += N) table[i] = -1;
         bool wrong = a.teacher_lse && !(fabsf(a.teacher_lse[row]) < INFINITY), any = false;
-        for (int j = threadIdx.x; j < top4; j += kThreads) {
+        for (int j = TEAM::id(); j < top4; j += N) {
             const int i = j < top ? a.index[row * top + j] : -1;
             const float v = j < top ? a.top_logits[row * top + j] / a.temperature : 0.f;
             const bool in = i >= 0 && i < a.vocab;
@@ -144,12 +174,12 @@ struct Teacher {
             index[j] = in ? i : -1;
             logp[j] = in ? v : -INFINITY;
         }
-        *empty = !__syncthreads_or(any);
-        *bad = __syncthreads_or(wrong) && !*empty;
+        *empty = !TEAM::any(any);
+        *bad = TEAM::any(wrong) && !*empty;
     }
-    // All threads, after read_entries and before a barrier: marks the indices that more than one entry has.
+    // After read_entries: marks the indices that more than one entry has.
     __device__ void mark_twins() const {
-        for (int j = threadIdx.x; j < top; j += kThreads) {
+        for (int j = TEAM::id(); j < top; j += N) {
             const int v = index[j];
             if (v < 0) continue;
             for (unsigned h = first_slot(v);; ++h) {                         // half of the slots stay free
@@ -170,34 +200,28 @@ struct Teacher {
     }
     static constexpr int kTwin = 1 << 30;        // above every column
     __device__ static unsigned first_slot(int v) { return (unsigned(v) * 2654435761u) >> 7; }
-    // One warp, after read_entries: log p and p; P = sum p.
-    __device__ float weights(const DistillArgs& a, int64_t row) const {
-        const int lane = threadIdx.x & 31;
+    // After read_entries: log p and p of this thread's entries; P = sum p.  `red`: 3 N / 32 values.
+    __device__ float weights(const DistillArgs& a, int64_t row, float* red) const {
         float c;
         if (a.teacher_lse) {
             c = a.teacher_lse[row];
         } else {
             float high = -INFINITY, sum = 0.f;
-            for (int j = lane; j < top; j += 32) high = fmaxf(high, logp[j]);
-#pragma unroll
-            for (int s = 16; s >= 1; s >>= 1) high = fmaxf(high, __shfl_xor_sync(kFullMask, high, s));
-            for (int j = lane; j < top; j += 32) sum += expf(logp[j] - high);
-#pragma unroll
-            for (int s = 16; s >= 1; s >>= 1) sum += __shfl_xor_sync(kFullMask, sum, s);
-            c = high + logf(sum);
+            for (int j = TEAM::id(); j < top; j += N) high = fmaxf(high, logp[j]);
+            high = TEAM::reduce(high, red, Larger());
+            for (int j = TEAM::id(); j < top; j += N) sum += expf(logp[j] - high);
+            c = high + logf(TEAM::reduce(sum, red + N / 32, Plus()));
         }
         float total = 0.f;
-        for (int j = lane; j < top4; j += 32) {
+        for (int j = TEAM::id(); j < top4; j += N) {
             const float l = logp[j] - c, w = expf(l);
             logp[j] = l;
             p[j] = w;
             total += w;
         }
-#pragma unroll
-        for (int s = 16; s >= 1; s >>= 1) total += __shfl_xor_sync(kFullMask, total, s);
-        return total;
+        return TEAM::reduce(total, red + 2 * (N / 32), Plus());
     }
-    // All threads: f(j, v, sum of the weights of index v) for the entries in a slice, each index once.
+    // Threads 0 to kThreads - 1: f(j, v, sum of the weights of index v) for the entries in a slice, each index once.
     template <typename S, typename F>
     __device__ __forceinline__ void each(const S& slice, F f) const {
         for (int j = threadIdx.x; j < top; j += kThreads) {
@@ -219,6 +243,13 @@ struct Teacher {
         }
     }
 };
+
+int slots_of(int top) {
+    int n = 32;
+    while (n < 2 * top) n *= 2;
+    return n;
+}
+unsigned teacher_bytes(int top) { return unsigned((top + 3) / 4 * 4 * 12 + slots_of(top) * 4); }
 
 // Gradient 0 for the columns of a slice.
 template <typename T>
@@ -279,187 +310,225 @@ struct Share {
     double term;
 };
 
-// Loss (STEP: and gradient).  A cluster of `slices` CTAs to a row.
+// Loss (STEP: and gradient).  A cluster of `slices` CTAs to a row.  Eight warps work on
+// the slice; four more start its copy and see to the teacher's entries meanwhile.
 template <typename T, bool STEP>
-__global__ void __launch_bounds__(kThreads) loss_kernel(const DistillArgs a, const int slices, const int chunk_room) {
+__global__ void __launch_bounds__(kThreads + kTeachers, 3)
+loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const int slots) {
     extern __shared__ __align__(128) uint4 chunk[];
-    __shared__ Share share[kMaxSlices], part[kWarps];
+    __shared__ Share share[kMaxSlices];
+    __shared__ Norm part[kWarps];
+    __shared__ double term_of_slice;
     __shared__ float extra[2 * Slice<T>::kPer];
     __shared__ float total_of_p;
-    __shared__ uint64_t bar[kSegments];
+    __shared__ int flags;                        // 1: no entry, 2: the row fails
+    __shared__ uint64_t bar[kMaxSegments];
+    __shared__ float red[3 * kTeachers / 32];
+    __shared__ double red64[kTeachers / 32];
     constexpr int kPer = Slice<T>::kPer;
-    constexpr int kGroup = 4;                    // chunks that share a step of the running maximum
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int64_t row = blockIdx.x / slices;
+    const int64_t row = blockIdx.x / unsigned(slices);
     const int rank = slices > 1 ? int(cluster_rank()) : 0;
     const auto* z = static_cast<const typename T::storage*>(a.logits) + row * a.ld;
     auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
     const Slice<T> slice(z, int(a.vocab), rank, slices);
-    Teacher teacher(chunk + chunk_room, a.top);
+    using Extra = Team<kThreads, kTeachers>;
+    Teacher<Extra, kTeachers> teacher(chunk + chunk_room, a.top, slots);
     const bool vec = STEP && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     if (slices > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");      // every CTA of the row has begun
-
-    auto segment = [&](int i) { return slice.chunks * i / kSegments; };           // first chunk of segment i
-    auto start_copy = [&] {                      // one thread
-        for (int i = 0; i < kSegments; ++i) {
-            const int c = segment(i), n = segment(i + 1) - c;
-            mbar_arrive_expect_tx(bar + i, n * 16);
-            if (n > 0) bulk_load(chunk + c, z + slice.first + c * kPer, n * 16, bar + i);
-        }
-    };
-    if (t == 0) {
-        for (int i = 0; i < kSegments; ++i) mbar_init(bar + i, 1);
-        mbar_init_fence();
-        if (!STEP) start_copy();
-    }
     if (t < slice.extras()) extra[t] = read<T>(z + slice.extra(t));
-    bool empty, bad;
-    teacher.read_entries(a, row, &empty, &bad);
-    if (STEP && (empty || bad)) {                // the logits are not read
-        if (slices > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-        write_zeros<T>(g, slice, vec);
-        if (t == 0 && rank == 0) {
-            a.loss[row] = bad ? NAN : 0.f;
-            if (bad) atomicAdd(&g_row_failures, 1ull);
-        }
-        return;
+    if (t == kThreads) {
+        for (int i = 0; i < kMaxSegments; ++i) mbar_init(bar + i, 1);
+        mbar_init_fence();
     }
-    if (STEP && t == 0) start_copy();
-    if (STEP) teacher.mark_twins();
-    if (warp == 0 && !empty) {                   // the others wait for the copy meanwhile
-        const float total = teacher.weights(a, row);
-        if (lane == 0) total_of_p = total;
-    }
-
-    // one pass over the slice; a NaN or +inf anywhere makes the sum NaN
-    const float inv_t = 1.f / a.temperature, scale2 = inv_t * kLog2E;
-    const float2 by2 = make_float2(scale2, scale2);
-    Norm norm{-INFINITY, 0.f};
-    bool stalled = false;
-    for (int i = 0; i < kSegments; ++i) {
-        if (!mbar_wait_bounded(bar + i, 0)) stalled = true;
-        const int end = segment(i + 1);
-        for (int c = segment(i) + t; c < end; c += kGroup * kThreads) {
-            uint4 v[kGroup];
-            float high = norm.high;
-#pragma unroll
-            for (int k = 0; k < kGroup; ++k) {
-                if (c + k * kThreads >= end) break;
-                v[k] = chunk[c + k * kThreads];
-                if constexpr (std::is_same<T, BF16>::value) {
-                    uint32_t m, n;
-                    asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(v[k].x), "r"(v[k].y));
-                    asm("max.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(v[k].z), "r"(v[k].w));
-                    asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
-                    high = fmaxf(high, fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u)));
-                } else {
-                    high = fmaxf(high, fmaxf(fmaxf(__uint_as_float(v[k].x), __uint_as_float(v[k].y)),
-                                             fmaxf(__uint_as_float(v[k].z), __uint_as_float(v[k].w))));
-                }
-            }
-            const float base = finite_base(high);
-            const float2 minus = make_float2(-base, -base);
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < kGroup; ++k) {
-                if (c + k * kThreads >= end) break;
-#pragma unroll
-                for (int q = 0; q < kPer / 2; ++q) {
-                    const float2 x = mul2(add2(pair_of<T>(v[k], q), minus), by2);
-                    sum = add2(sum, make_float2(ex2(x.x), ex2(x.y)));
-                }
-            }
-            norm.sum = fmaf(norm.sum, ex2((norm.high - base) * scale2), sum.x + sum.y);
-            norm.high = high;
-        }
-    }
-    if (t < slice.extras()) {
-        const float x = extra[t];
-        const Norm two[2] = {norm, Norm{x == x ? x : -INFINITY, x == x ? (x == -INFINITY ? 0.f : 1.f) : x}};
-        norm = join(2, scale2, [&](int k) { return two[k]; });
-    }
-    if (stalled) norm.sum = NAN;
-    float high = norm.high;
-#pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) high = fmaxf(high, __shfl_xor_sync(kFullMask, high, s));
-    norm.sum *= ex2((norm.high - finite_base(high)) * scale2);
-    norm.high = high;
-#pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) norm.sum += __shfl_xor_sync(kFullMask, norm.sum, s);
     __syncthreads();
 
-    // sum_j p_j (log p_j - z_j / T) of the entries in this slice
+    const int segments = (slice.chunks + kSegment - 1) / kSegment;
     auto logit_at = [&](int v) {
         if (v < slice.head) return extra[v];
         if (v >= slice.first && v < slice.first + slice.chunks * kPer)
             return read<T>(reinterpret_cast<const typename T::storage*>(chunk) + (v - slice.first));
         return extra[slice.head + v - (slice.vocab - slice.tail)];
     };
-    double term = 0.0;
-    if (!empty)
-        for (int j = t; j < a.top; j += kThreads) {
-            const int v = teacher.index[j];
-            const float w = teacher.p[j];
-            if (v >= 0 && w > 0.f && slice.has(v))
-                term += double(w) * (double(teacher.logp[j]) - double(logit_at(v)) * a.inv_t);
+    const float inv_t = 1.f / a.temperature, scale2 = inv_t * kLog2E;
+    const float2 by2 = make_float2(scale2, scale2);
+    bool stalled = false;
+    if (warp >= kWarps) {
+        bool empty, bad;
+        auto start_copy = [&](bool bytes) {      // segments past the slice complete at once, as all do without bytes
+            if (t != kThreads) return;
+            for (int i = 0; i < kMaxSegments; ++i) {
+                const int c = i * kSegment, left = slice.chunks - c;
+                const int n = !bytes || left < 0 ? 0 : left < kSegment ? left : kSegment;
+                mbar_arrive_expect_tx(bar + i, n * 16);
+                if (n > 0) bulk_load(chunk + c, z + slice.first + c * kPer, n * 16, bar + i);
+            }
+        };
+        if (!STEP) start_copy(true);
+        teacher.read_entries(a, row, &empty, &bad);
+        if (t == kThreads) flags = (empty ? 1 : 0) | (bad ? 2 : 0);
+        if (STEP) start_copy(!empty && !bad);    // otherwise the logits are not read
+        if (!empty && !(STEP && bad)) {
+            if (STEP) teacher.mark_twins();
+            const float total = teacher.weights(a, row, red);
+            for (int i = 0; i < segments; ++i)
+                if (!mbar_wait_bounded(bar + i, 0)) stalled = true;
+            // sum_j p_j (log p_j - z_j / T) of the entries in this slice
+            double term = 0.0;
+            for (int j = Extra::id(); j < a.top; j += kTeachers) {
+                const int v = teacher.index[j];
+                const float w = teacher.p[j];
+                if (v >= 0 && w > 0.f && slice.has(v))
+                    term += double(w) * (double(teacher.logp[j]) - double(logit_at(v)) * a.inv_t);
+            }
+            term = Extra::reduce(term, red64, Plus());
+            if (t == kThreads) {
+                total_of_p = total;
+                term_of_slice = term;
+            }
         }
+    } else {
+        // one pass over the slice; a NaN or +inf anywhere makes the sum NaN
+        Norm norm{-INFINITY, 0.f};
+        auto take = [&](const uint4* v, auto count) {
+            constexpr int n = decltype(count)::value;
+            float high;
+            if constexpr (std::is_same<T, BF16>::value) {
+                uint32_t m = v[0].x;
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) term += __shfl_xor_sync(kFullMask, term, s);
-    if (lane == 0) part[warp] = Share{norm, term};
+                for (int k = 0; k < n; ++k) {
+                    uint32_t x, y;
+                    asm("max.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(v[k].x), "r"(v[k].y));
+                    asm("max.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(v[k].z), "r"(v[k].w));
+                    asm("max.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(y));
+                    asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(x));
+                }
+                high = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+            } else {
+                high = __uint_as_float(v[0].x);
+#pragma unroll
+                for (int k = 0; k < n; ++k)
+                    high = fmaxf(fmaxf(high, fmaxf(__uint_as_float(v[k].x), __uint_as_float(v[k].y))),
+                                 fmaxf(__uint_as_float(v[k].z), __uint_as_float(v[k].w)));
+            }
+            high = fmaxf(norm.high, high);
+            const float base = finite_base(high);
+            const float2 minus = make_float2(-base, -base);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int k = 0; k < n; ++k)
+#pragma unroll
+                for (int q = 0; q < kPer / 2; ++q) {
+                    const float2 x = mul2(add2(pair_of<T>(v[k], q), minus), by2);
+                    sum[q & 1] = add2(sum[q & 1], make_float2(ex2(x.x), ex2(x.y)));
+                }
+            const float2 both = add2(sum[0], sum[1]);
+            norm.sum = fmaf(norm.sum, ex2((norm.high - base) * scale2), both.x + both.y);
+            norm.high = high;
+        };
+        for (int i = 0; i < segments; ++i) {
+            if (!mbar_wait_bounded(bar + i, 0)) stalled = true;
+            if (STEP && flags) break;
+            const uint4* from = chunk + i * kSegment + t;
+            const int left = slice.chunks - i * kSegment - t;
+            if (left > (kGroup - 1) * kThreads) {
+                uint4 v[kGroup];
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) v[k] = from[k * kThreads];
+                take(v, std::integral_constant<int, kGroup>());
+            } else {
+                for (int k = 0; k * kThreads < left; ++k) {
+                    const uint4 v = from[k * kThreads];
+                    take(&v, std::integral_constant<int, 1>());
+                }
+            }
+        }
+        if (t < slice.extras()) {
+            const float x = extra[t];
+            const Norm two[2] = {norm, Norm{x == x ? x : -INFINITY, x == x ? (x == -INFINITY ? 0.f : 1.f) : x}};
+            norm = join(2, scale2, [&](int k) { return two[k]; });
+        }
+        if (stalled) norm.sum = NAN;
+        float high = norm.high;
+#pragma unroll
+        for (int s = 16; s >= 1; s >>= 1) high = fmaxf(high, __shfl_xor_sync(kFullMask, high, s));
+        norm.sum *= ex2((norm.high - finite_base(high)) * scale2);
+#pragma unroll
+        for (int s = 16; s >= 1; s >>= 1) norm.sum += __shfl_xor_sync(kFullMask, norm.sum, s);
+        if (lane == 0) part[warp] = Norm{high, norm.sum};
+    }
     __syncthreads();
-    auto sum_terms = [](const Share* s, int n) {
-        double x = s[0].term;
-        for (int k = 1; k < n; ++k) x += s[k].term;
-        return x;
-    };
-    norm = join(kWarps, scale2, [&](int k) { return part[k].norm; });
+    const bool empty = flags & 1;
+    bool failed = flags & 2;
+    if (STEP && flags) {
+        if (slices > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        if (warp < kWarps) write_zeros<T>(g, slice, vec);
+        if (t == 0 && rank == 0) {
+            a.loss[row] = failed ? NAN : 0.f;
+            if (failed) atomicAdd(&g_row_failures, 1ull);
+        }
+        return;
+    }
+
+    Norm norm = join(kWarps, scale2, [&](int k) { return part[k]; });
+    double term = term_of_slice;
     if (slices > 1) {
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-        if (t < slices) {
-            const uint32_t to = cluster_addr(smem_u32(share + rank), t);
-            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(norm.high), "f"(norm.sum) : "memory");
-            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to + 8), "d"(sum_terms(part, kWarps)) : "memory");
+        if (warp == 0) {
+            if (t < slices) {
+                const uint32_t to = cluster_addr(smem_u32(share + rank), t);
+                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(norm.high), "f"(norm.sum) : "memory");
+                asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to + 8), "d"(term) : "memory");
+            }
+            __syncwarp();
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        } else {
+            asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
         }
-        cluster_sync();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         norm = join(slices, scale2, [&](int k) { return share[k].norm; });
+        term = 0.0;
+        for (int k = 0; k < slices; ++k) term += share[k].term;
     }
     const float m = norm.high;
-    const bool failed = bad || (!empty && !(fabsf(m) < INFINITY && norm.sum < INFINITY));
-    if (t == 0 && rank == 0) {
+    failed = failed || (!empty && !(fabsf(m) < INFINITY && norm.sum < INFINITY));
+    if (t == kThreads && rank == 0) {
         const double lse = m == -INFINITY ? double(m + norm.sum)              // no finite logit: -inf, or NaN
                                           : double(m) * a.inv_t + log_sum(norm.sum);
-        const double all = slices > 1 ? sum_terms(share, slices) : sum_terms(part, kWarps);
         a.loss[row] = failed ? NAN : empty ? 0.f
-                      : float(double(a.temperature) * double(a.temperature) * (all + double(total_of_p) * lse));
+                      : float(double(a.temperature) * double(a.temperature) * (term + double(total_of_p) * lse));
         if (!STEP) a.lse[row] = failed ? NAN : float(lse);
         if (failed) atomicAdd(&g_row_failures, 1ull);
     }
     if constexpr (STEP) {
         const float by = a.temperature * (a.weight ? a.weight[row] : 1.f);
         if (failed || by == 0.f) {
-            write_zeros<T>(g, slice, vec);
+            if (warp < kWarps) write_zeros<T>(g, slice, vec);
             return;
         }
         const float scale = by * total_of_p / norm.sum;
         auto at = [&](float x) { return scale * ex2((x - m) * scale2); };
-        const float2 minus_m = make_float2(-m, -m), scale_2 = make_float2(scale, scale);
+        if (warp < kWarps) {
+            const float2 minus_m = make_float2(-m, -m), scale_2 = make_float2(scale, scale);
 #pragma unroll 4
-        for (int c = t; c < slice.chunks; c += kThreads)
-            write_chunk<T>(g + slice.first + c * kPer, chunk[c], vec, [&](float2 x) {
-                x = mul2(add2(x, minus_m), by2);
-                return mul2(make_float2(ex2(x.x), ex2(x.y)), scale_2);
-            });
-        if (t < slice.extras()) write<T>(g + slice.extra(t), at(extra[t]));
+            for (int c = t; c < slice.chunks; c += kThreads)
+                write_chunk<T>(g + slice.first + c * kPer, chunk[c], vec, [&](float2 x) {
+                    x = mul2(add2(x, minus_m), by2);
+                    return mul2(make_float2(ex2(x.x), ex2(x.y)), scale_2);
+                });
+            if (t < slice.extras()) write<T>(g + slice.extra(t), at(extra[t]));
+        }
         __syncthreads();                         // the entries' columns are written again
-        teacher.each(slice, [&](int, int v, float w) { write<T>(g + v, at(logit_at(v)) - by * w); });
+        if (warp < kWarps)
+            teacher.each(slice, [&](int, int v, float w) { write<T>(g + v, at(logit_at(v)) - by * w); });
     }
 }
 
 // The gradient from lse; blockIdx.x is a row's slice.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, const int slices) {
+__global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, const int slices, const int slots) {
     extern __shared__ __align__(128) uint4 room[];
-    __shared__ float total_of_p;
+    __shared__ float red[3 * kWarps];
     constexpr int kPer = Slice<T>::kPer;
     constexpr int kAhead = 4;                    // chunks of a thread in flight
     const int t = threadIdx.x;
@@ -468,13 +537,13 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     const auto* z = static_cast<const typename T::storage*>(a.logits) + row * a.ld;
     auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
     const Slice<T> slice(z, int(a.vocab), rank, slices);
-    Teacher teacher(room, a.top);
+    Teacher<Team<0, kThreads>, kThreads> teacher(room, a.top, slots);
     float* target = teacher.logp;                // log p is not needed here
     const bool vec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
-    bool empty, bad;
-    teacher.read_entries(a, row, &empty, &bad);
     const float lse = a.lse[row];
     const float by = a.temperature * (a.weight ? a.weight[row] : 1.f);
+    bool empty, bad;
+    teacher.read_entries(a, row, &empty, &bad);
     bad = bad || (!empty && !(fabsf(lse) < INFINITY));
     if (bad && rank == 0 && t == 0) atomicAdd(&g_row_failures, 1ull);
     if (bad || empty || by == 0.f) {
@@ -490,12 +559,9 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     };
     load(t);                                     // on their way while the weights are made
     teacher.mark_twins();
-    if (t < 32) {
-        const float total = teacher.weights(a, row);
-        if (t == 0) total_of_p = total;
-    }
+    const float total = teacher.weights(a, row, red);
     __syncthreads();
-    const float inv_t = 1.f / a.temperature, scale = by * total_of_p;
+    const float inv_t = 1.f / a.temperature, scale = by * total;
     auto at = [&](float x) { return scale * ex2(fmaf(x, inv_t, -lse) * kLog2E); };
     // the entries' gradients before anything is written: grad may be the logits
     teacher.each(slice, [&](int j, int c, float w) { target[j] = at(read<T>(z + c)) - by * w; });
@@ -530,12 +596,12 @@ cudaError_t launch_loss(const DistillArgs& a, cudaStream_t st) {
     const int64_t row_bytes = a.vocab * int64_t(sizeof(typename T::storage));
     const int slices = slices_of(a.rows, row_bytes);
     const int chunk_room = int((row_bytes / 16 + slices - 1) / slices);
-    const unsigned bytes = unsigned(chunk_room * 16) + Teacher::bytes(a.top);
+    const unsigned bytes = unsigned(chunk_room * 16) + teacher_bytes(a.top);
     cudaError_t e = cudaFuncSetAttribute(loss_kernel<T, STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.rows * slices));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads + kTeachers);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -544,7 +610,7 @@ cudaError_t launch_loss(const DistillArgs& a, cudaStream_t st) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = slices > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, loss_kernel<T, STEP>, a, slices, chunk_room);
+    return cudaLaunchKernelEx(&cfg, loss_kernel<T, STEP>, a, slices, chunk_room, slots_of(a.top));
 }
 
 template <typename T>
@@ -553,7 +619,7 @@ cudaError_t launch_grad(const DistillArgs& a, cudaStream_t st) {
     const int64_t row_bytes = a.vocab * int64_t(sizeof(typename T::storage));
     const int slices = a.rows >= 296 ? int((row_bytes + kSliceBytes - 1) / kSliceBytes)
                                      : int((row_bytes + kSliceBytes / 8 - 1) / (kSliceBytes / 8));
-    grad_kernel<T><<<unsigned(a.rows * slices), kThreads, Teacher::bytes(a.top), st>>>(a, slices);
+    grad_kernel<T><<<unsigned(a.rows * slices), kThreads, teacher_bytes(a.top), st>>>(a, slices, slots_of(a.top));
     return cudaGetLastError();
 }
 
