@@ -120,6 +120,21 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
         ::"r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
 }
 
+// Polls as mbar_wait_bounded does, each poll asleep for up to 2 us: for warps that have nothing
+// else to do while others work.
+__device__ __forceinline__ bool mbar_sleep_bounded(uint64_t* bar, unsigned parity) {
+    for (unsigned k = 0; k < kTmaPolls; ++k) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done) : "r"(smem_u32(bar)), "r"(parity), "r"(2000u) : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+
 // ---- copies and clusters ----------------------------------------------------------------
 
 // `bytes` (a multiple of 16, both ends 16-byte aligned) from global memory into this CTA.
