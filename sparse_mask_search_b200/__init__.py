@@ -335,13 +335,14 @@ def _strided(t, name, types):
     if t.dtype not in types:
         raise TypeError(f"{name} must be {' or '.join(str(x) for x in types)}, got {t.dtype}")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have dense rows")
-    if rows <= 1:
-        return max(cols, t.stride(0))
-    if t.stride(0) < cols:
-        raise ValueError(f"{name} must have rows that do not overlap")
-    return t.stride(0)
+    if ld < cols:
+        if rows > 1:
+            raise ValueError(f"{name} must have rows that do not overlap")
+        return cols
+    return ld
 
 
 def _dense(t, name, dtype, shape, device):
@@ -386,9 +387,7 @@ def _needs_guard(device, stream):
 
 def _new_codes(rows, cols, device):
     import torch
-    ld = (cols + 15) // 16 * 16
-    t = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device)
-    return t if ld == cols else t[:, :cols]
+    return torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=torch.float8_e4m3fn, device=device)
 
 
 def _codes(t, name, device, shape=None):
@@ -409,7 +408,13 @@ def _codes(t, name, device, shape=None):
 
 def _new_scales(rows, cols, device):
     import torch
-    return torch.empty(scale_shape(rows, cols), dtype=torch.uint8, device=device)
+    k, t = (cols + 511) // 512, (rows + 127) // 128
+    return torch.empty_strided((k, t, 512), (t * 512, 512, 1), dtype=torch.uint8, device=device)
+
+
+def _new_row_values(rows, device):
+    import torch
+    return torch.empty_strided((rows,), (1,), dtype=torch.float32, device=device)
 
 
 def _float_types():
@@ -496,7 +501,7 @@ def _output(out, rows, cols, dtype, device):
     if out is None:
         if dtype not in _float_types():
             raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
-        return torch.empty((rows, cols), dtype=dtype, device=device), max(cols, 1)
+        return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device), cols
     ldo = _strided(out, "out", _float_types())
     if out.device != device:
         raise ValueError(f"out must be on {device}")
@@ -567,7 +572,7 @@ def _distill_grad_args(logits, weight, grad):
     if weight is not None:
         _dense(weight, "weight", torch.float32, (rows,), logits.device)
     if grad is None:
-        grad, ldg = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device), vocab
+        grad, ldg = torch.empty_strided((rows, vocab), (vocab, 1), dtype=logits.dtype, device=logits.device), vocab
     else:
         ldg = _strided(grad, "grad", (logits.dtype,))
         if grad.shape != logits.shape or grad.device != logits.device:
@@ -584,13 +589,11 @@ def tsenor_distill_loss(logits, index, top_logits, temperature: float = 1.0, tea
     softmax of top_logits / T over the row's entries, or, with teacher_lse (rows,)
     float32, exp(top_logits / T - teacher_lse).  lse is what tsenor_distill_grad takes.
     """
-    import torch
     if logits.is_cuda and _needs_guard(logits.device, stream):
         with _on(logits.device, stream):
             return tsenor_distill_loss(logits, index, top_logits, temperature, teacher_lse)
     args = _distill_args(logits, index, top_logits, temperature, teacher_lse)
-    loss = torch.empty((logits.shape[0],), dtype=torch.float32, device=logits.device)
-    lse = torch.empty_like(loss)
+    loss, lse = _new_row_values(logits.shape[0], logits.device), _new_row_values(logits.shape[0], logits.device)
     _launch(lib().tsenor_distill_loss, logits.device, *args, loss.data_ptr(), lse.data_ptr())
     return loss, lse
 
@@ -602,13 +605,12 @@ def tsenor_distill_step(logits, index, top_logits, temperature: float = 1.0, tea
     weight: (rows,) float32, default 1: the upstream gradient of each row's loss.
     grad: optional output like the logits, which may be the logits themselves.
     """
-    import torch
     if logits.is_cuda and _needs_guard(logits.device, stream):
         with _on(logits.device, stream):
             return tsenor_distill_step(logits, index, top_logits, temperature, teacher_lse, weight, grad)
     args = _distill_args(logits, index, top_logits, temperature, teacher_lse)
     grad, weight_ptr, ldg = _distill_grad_args(logits, weight, grad)
-    loss = torch.empty((logits.shape[0],), dtype=torch.float32, device=logits.device)
+    loss = _new_row_values(logits.shape[0], logits.device)
     _launch(lib().tsenor_distill_step, logits.device, *args, weight_ptr, loss.data_ptr(), grad.data_ptr(), ldg)
     return loss, grad
 
