@@ -38,7 +38,7 @@ constexpr int kPad = 132;                        // floats to a staged row: 16-b
 // The products issue and load loops may wait for as long as a tile's sums take.
 __device__ __forceinline__ bool wait_long(uint64_t* bar, unsigned parity, int64_t blocks) {
     for (int64_t i = 0; i <= blocks / 64; ++i)
-        if (mbar_wait_bounded(bar, parity)) return true;
+        if (mbar_sleep_bounded(bar, parity)) return true;
     return false;
 }
 
@@ -77,14 +77,20 @@ __device__ __forceinline__ void store4(const MatmulArgs& p, int64_t r, int64_t c
     }
 }
 
+// Mask words of a row for 128 columns from c on; asked for before the sums are ready.
+__device__ __forceinline__ void load_mask(const MatmulArgs& p, int64_t r, int64_t c, uint32_t (&w)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = p.mask && r < p.m && c + 32 * i < p.n ? __ldg(p.mask + r * p.wpr + c / 32 + i) : 0xffffffffu;
+}
+__device__ __forceinline__ void apply_mask(uint32_t w, uint32_t (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = (w >> i) & 1u ? v[i] : 0u;
+}
+
 // 32 sums of row r from column c on, held by one thread.
 template <bool BF16OUT>
-__device__ __forceinline__ void store_row(const MatmulArgs& p, int64_t r, int64_t c, uint32_t (&v)[32]) {
-    if (p.mask) {
-        const uint32_t w = c < p.n ? __ldg(p.mask + r * p.wpr + c / 32) : 0u;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = (w >> i) & 1u ? v[i] : 0u;
-    }
+__device__ __forceinline__ void store_row(const MatmulArgs& p, int64_t r, int64_t c, const uint32_t (&v)[32]) {
     if constexpr (BF16OUT) {
         uint16_t* o = static_cast<uint16_t*>(p.out) + r * p.ldo + c;
 #pragma unroll
@@ -123,7 +129,7 @@ __device__ __forceinline__ void store_row(const MatmulArgs& p, int64_t r, int64_
 // The same for rows that do not start on 32 bytes: the warp's 32 x 32 sums turn
 // through shared memory, so that a store instruction covers one row.
 template <bool BF16OUT>
-__device__ __forceinline__ void store_turned(const MatmulArgs& p, int64_t r0, int64_t c, uint32_t (&v)[32], float* staged) {
+__device__ __forceinline__ void store_turned(const MatmulArgs& p, int64_t r0, int64_t c, const uint32_t (&v)[32], float* staged) {
     const int lane = threadIdx.x & 31;
     __syncwarp();
 #pragma unroll
@@ -131,9 +137,8 @@ __device__ __forceinline__ void store_turned(const MatmulArgs& p, int64_t r0, in
     __syncwarp();
     if (c + lane >= p.n) return;
     for (int i = 0; i < 32 && r0 + i < p.m; ++i) {
-        float x = staged[i * 33 + lane];
+        const float x = staged[i * 33 + lane];
         const int64_t r = r0 + i;
-        if (p.mask && !((__ldg(p.mask + r * p.wpr + c / 32) >> lane) & 1u)) x = 0.f;
         if constexpr (BF16OUT) static_cast<uint16_t*>(p.out)[r * p.ldo + c + lane] = to_bf16(x);
         else static_cast<float*>(p.out)[r * p.ldo + c + lane] = x;
     }
@@ -272,16 +277,18 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         float* staged = reinterpret_cast<float*>(smem);
         unsigned n = 0;
         for (int64_t t = first; t < tiles; t += step, ++n) {
+            const int64_t r0 = t % p.tiles_m * kTile + quarter * 32, c0 = t / p.tiles_m * kTile;
+            uint32_t mask[4];
+            if constexpr (!SPLIT) load_mask(p, r0 + lane, c0, mask);
             if (!wait_long(ready + (n & 1), (n >> 1) & 1, k1 - k0)) { stalled = true; break; }
             tmem_fence_after();
-            const int64_t r0 = t % p.tiles_m * kTile + quarter * 32, c0 = t / p.tiles_m * kTile;
             const uint32_t d = *reinterpret_cast<volatile uint32_t*>(slot) + (uint32_t(quarter * 32) << 16) + (n & 1) * kTile;
             if (r0 < p.m) {
-#pragma unroll 1
+#pragma unroll
                 for (int c = 0; c < kTile; c += 32) {
                     uint32_t v[32];
                     tmem_load32(d + c, v);
-                    tmem_wait_load();
+                    tmem_wait_load(v);
                     if constexpr (SPLIT) {
                         if (r0 + lane < p.m) {
 #pragma unroll
@@ -290,6 +297,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                                     make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                         }
                     } else if (c0 + c < p.n) {
+                        apply_mask(mask[c / 32], v);
                         if (p.vec) {
                             if (r0 + lane < p.m) store_row<BF16OUT>(p, r0 + lane, c0 + c, v);
                         } else {
@@ -314,15 +322,32 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         const int64_t tm = first % p.tiles_m, tn = first / p.tiles_m;
         const int rows = int(p.m - tm * kTile < kTile ? p.m - tm * kTile : kTile);
         const uint32_t base = smem_u32(smem);
-        for (int u = int(rank) * kThreads + threadIdx.x; u < rows * (kTile / 4); u += split * kThreads) {
-            const int r = u / (kTile / 4), c = u % (kTile / 4) * 4;
-            if (tn * kTile + c >= p.n) continue;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        // four sums of four columns at a time, so that their loads are in flight together
+        constexpr int kAhead = 4;
+        const int units = rows * (kTile / 4), step_u = split * kThreads;
+        for (int u0 = int(rank) * kThreads + threadIdx.x; u0 < units; u0 += kAhead * step_u) {
+            float4 v[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int q = 0; q < split; ++q) {
-                const float4 w = cluster_load4(cluster_addr(base + (r * kPad + c) * 4, q));
-                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+                float4 w[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int u = u0 + i * step_u;
+                    if (u < units)
+                        w[i] = cluster_load4(cluster_addr(base + (u / (kTile / 4) * kPad + u % (kTile / 4) * 4) * 4, q));
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    if (u0 + i * step_u < units)
+                        v[i] = make_float4(v[i].x + w[i].x, v[i].y + w[i].y, v[i].z + w[i].z, v[i].w + w[i].w);
             }
-            store4<BF16OUT>(p, tm * kTile + r, tn * kTile + c, v);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int u = u0 + i * step_u;
+                const int r = u / (kTile / 4), c = u % (kTile / 4) * 4;
+                if (u < units && tn * kTile + c < p.n) store4<BF16OUT>(p, tm * kTile + r, tn * kTile + c, v[i]);
+            }
         }
         cluster_sync();                          // a peer's shared memory lives until all have read it
     }
@@ -336,15 +361,15 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 // 512 columns of tensor memory, so the second one starts at column 240: its
 // product may start once the 32 columns that hold the overlap have been read, which
 // the epilogue does first.
-constexpr int kPairThreads = 256;                // warps: 0 loads, 1 products, 2 tensor memory, 4-7 epilogue
+constexpr int kPairThreads = 384;                // warps: 0 loads, 1 products, 2 tensor memory, 4 to 11 epilogue
 constexpr int kPairTile = 256;
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
 constexpr int kSecond = 240, kScaleA = 496, kScaleB = 500;
 constexpr int kGroupM = 16;                      // tiles of 256 rows walked together, so that B is read from L2
 
 struct PairSmem {
     static constexpr unsigned a = 0, b = kPairStages * kTileBytes, s = 2 * b, staged = s + kPairStages * 3 * kScaleBytes,
-                              bars = staged + 4 * 32 * 33 * 4, bytes = bars + (2 * kPairStages + 3) * 8 + 16;
+                              bars = staged + 8 * 32 * 33 * 4, bytes = bars + (2 * kPairStages + 3) * 8 + 16;
 };
 
 // Tile t of the walk: groups of kGroupM tile rows, column by column within a group.
@@ -380,7 +405,7 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         }
         mbar_init(ready, 1);
         mbar_init(ready + 1, 1);
-        mbar_init(room, 8);                      // the epilogue warps of both CTAs; used in rank 0
+        mbar_init(room, 16);                     // the epilogue warps of both CTAs; used in rank 0
         mbar_init_fence();
     }
     if (warp == 2) tmem_alloc<2>(slot, 512);
@@ -461,33 +486,46 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             __syncwarp();
         }
     } else if (warp >= 4) {
-        const int quarter = warp & 3;
-        float* staged = reinterpret_cast<float*>(smem + PairSmem::staged) + quarter * 32 * 33;
+        // two warps to a quarter of the lanes, 128 columns each
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        float* staged = reinterpret_cast<float*>(smem + PairSmem::staged) + (warp - 4) * 32 * 33;
         const uint32_t room_bar = cluster_addr(smem_u32(room), 0);
         unsigned n = 0;
         for (int64_t t = first; t < tiles; t += step, ++n) {
-            if (!wait_long(ready + (n & 1), (n >> 1) & 1, blocks)) { stalled = true; break; }
-            tmem_fence_after();
             int64_t tm, tn;
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
-            const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + (n & 1 ? kSecond : 0);
-            const int64_t r0 = (tm * 2 + rank) * kTile + quarter * 32, c0 = tn * kPairTile;
-#pragma unroll 1
-            for (int q = 0; q < 8; ++q) {
-                const int c = (n & 1 ? q : 7 - q) * 32;      // the columns that the other accumulator shares first
-                uint32_t v[32];
-                tmem_load32(d + c, v);
-                tmem_wait_load();
-                if (q == 0) {
-                    tmem_fence_before();
-                    __syncwarp();
-                    if (lane == 0) cluster_arrive(room_bar);
-                }
-                if (c0 + c >= p.n) continue;
-                if (p.vec) {
-                    if (r0 + lane < p.m) store_row<BF16OUT>(p, r0 + lane, c0 + c, v);
-                } else {
-                    store_turned<BF16OUT>(p, r0, c0 + c, v, staged);
+            const int64_t r0 = (tm * 2 + rank) * kTile + quarter * 32, c0 = tn * kPairTile + half * kTile;
+            uint32_t mask[4];
+            load_mask(p, r0 + lane, c0, mask);
+            if (!wait_long(ready + (n & 1), (n >> 1) & 1, blocks)) { stalled = true; break; }
+            tmem_fence_after();
+            const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + (n & 1 ? kSecond : 0) + half * kTile;
+            // The half that shares columns with the other accumulator reads those first: the last
+            // chunk of the first accumulator, the first of the second one.  The other half is done with the
+            // tile before, which is all that the next product needs of it.
+            const bool shares = half == (n & 1 ? 0 : 1);
+            auto chunk = [&](int q) { return n & 1 ? q : 3 - q; };
+            auto leave = [&] {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) cluster_arrive(room_bar);
+            };
+            if (!shares) leave();
+            uint32_t v[2][32];
+            tmem_load32(d + chunk(0) * 32, v[0]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                tmem_wait_load(v[q & 1]);
+                if (q == 0 && shares) leave();
+                if (q < 3) tmem_load32(d + chunk(q + 1) * 32, v[(q + 1) & 1]);       // on its way during the stores
+                const int c = chunk(q) * 32;
+                if (c0 + c < p.n) {
+                    apply_mask(n & 1 ? mask[q] : mask[3 - q], v[q & 1]);
+                    if (p.vec) {
+                        if (r0 + lane < p.m) store_row<BF16OUT>(p, r0 + lane, c0 + c, v[q & 1]);
+                    } else {
+                        store_turned<BF16OUT>(p, r0, c0 + c, v[q & 1], staged);
+                    }
                 }
             }
         }
@@ -556,14 +594,6 @@ cudaError_t launch_pair(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8
     return cudaGetLastError();
 }
 
-// CTAs that share a tile's sum: as many as leave no SM with two (a kernel that
-// holds tensor memory runs one CTA to an SM), with two blocks of 128 each at least.
-int split_of(int64_t tiles, int64_t blocks) {
-    int split = 1;
-    while (split < 8 && tiles * (split + 1) <= kSms && blocks / (split + 1) >= 2) ++split;
-    return split;
-}
-
 template <bool SPLIT>
 cudaError_t launch_tiles(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int split,
                          cudaStream_t st) {
@@ -596,10 +626,29 @@ cudaError_t launch_tiles(MatmulArgs p, const uint8_t* a, int64_t lda, const uint
     return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, p, split);
 }
 
+// Which kernel: by the time that each would take, in nanoseconds, from a fit to measured calls with weights
+// from memory.  A wave is one tile for each SM (or pair of SMs), a block 128 of the summed axis.
+//   pair_kernel:           6300 + 318 a block and wave   (256 x 4096 x 4096: 16.5 us measured, 16.5 fitted;
+//                                                          2048 x 4096 x 4096: 28.7, 26.7)
+//   tile_kernel, persistent: 4300 + 235 a block and wave (256 x 4096 x 4096: 11.9, 11.8; 512 x 11008 x 4096: 27.7, 26.9)
+//   tile_kernel, split s:  the same for blocks / s, and 1300 + 200 s + 22 a row to join the shares (1 x 4096 x 4096, s = 4:
+//                          8.7, 8.3, and 11.5 unsplit; 256 x 4096 x 4096, s = 2: 12.6, 12.6).  A split
+//                          beyond one CTA to an SM never pays (1 x 4096 x 4096, s = 6: 14.9).
 cudaError_t launch(const MatmulArgs& p, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, cudaStream_t st) {
-    const int64_t blocks = (p.k + kTile - 1) / kTile;
-    if (p.m > kTile) return launch_pair(p, a, lda, b, ldb, st);
-    const int split = split_of(p.tiles_m * p.tiles_n, blocks);
+    const int64_t blocks = (p.k + kTile - 1) / kTile, tiles = p.tiles_m * p.tiles_n;
+    const int64_t pairs = ((p.m + kPairTile - 1) / kPairTile) * ((p.n + kPairTile - 1) / kPairTile);
+    const int64_t rows = p.m < kTile ? p.m : kTile;
+    const int64_t as_pairs = 6300 + 318 * blocks * ((pairs + kSms / 2 - 1) / (kSms / 2));
+    int64_t best = 4300 + 235 * blocks * ((tiles + kSms - 1) / kSms);
+    int split = 1;
+    for (int s = 2; s <= 8 && tiles * s <= kSms && blocks / s >= 2; ++s) {
+        const int64_t ns = 4300 + 235 * ((blocks + s - 1) / s) + 1300 + 200 * s + 22 * rows;
+        if (ns < best) {
+            best = ns;
+            split = s;
+        }
+    }
+    if (as_pairs < best) return launch_pair(p, a, lda, b, ldb, st);
     return split > 1 ? launch_tiles<true>(p, a, lda, b, ldb, split, st) : launch_tiles<false>(p, a, lda, b, ldb, 1, st);
 }
 
