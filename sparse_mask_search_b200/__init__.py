@@ -328,38 +328,47 @@ def scale_shape(rows: int, cols: int) -> tuple[int, int, int]:
     return (cols + 511) // 512, (rows + 127) // 128, 512
 
 
-def _strided(t, name, types):
-    """Row stride of a 2-D CUDA tensor whose rows are dense."""
+# Helpers of the calls below.  They are called for every launch of a decoded token, so they read each
+# attribute of a tensor once and import nothing that their caller has.
+
+def _rows(t, name, types):
+    """(rows, cols, row stride) of a 2-D CUDA tensor whose rows are dense."""
     if not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
     if t.dtype not in types:
         raise TypeError(f"{name} must be {' or '.join(str(x) for x in types)}, got {t.dtype}")
-    rows, cols = t.shape
-    ld, step = t.stride()
+    (rows, cols), (ld, step) = t.shape, t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have dense rows")
     if ld < cols:
         if rows > 1:
             raise ValueError(f"{name} must have rows that do not overlap")
-        return cols
-    return ld
+        ld = cols
+    return rows, cols, ld
 
 
 def _dense(t, name, dtype, shape, device):
+    """Pointer of a contiguous tensor of this type, shape and device."""
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {shape}")
+    return t.data_ptr()
 
 
-def _mask_pointer(mask, rows, cols, device):
-    import torch
-    if mask is None:
-        return None
-    _dense(mask, "mask", torch.int32, (rows, words_per_row(cols)), device)
-    return mask.data_ptr()
+def _codes(t, name, types, device):
+    """(rows, cols, row stride, pointer) of a codes tensor."""
+    rows, cols, ld = _rows(t, name, types)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if rows <= 1 or cols == 0:
+        ld = (cols + 15) // 16 * 16
+    ptr = t.data_ptr()
+    if ld % 16 or ptr % 16:
+        raise ValueError(f"{name} must have rows that start on 16 bytes (a row stride that is a multiple of 16)")
+    return rows, cols, ld, ptr
 
 
 @contextlib.contextmanager
@@ -372,54 +381,13 @@ def _on(device, stream):
         yield
 
 
-def _launch(fn, device, *args):
-    """fn(*args, stream) on the device's current stream."""
-    import torch
-    status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
-    if status:
-        _check(status)
-
-
-def _needs_guard(device, stream):
-    import torch
-    return stream is not None or torch.cuda.current_device() != device.index
-
-
-def _new_codes(rows, cols, device):
-    import torch
+def _new_codes(torch, rows, cols, device):
     return torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=torch.float8_e4m3fn, device=device)
 
 
-def _codes(t, name, device, shape=None):
-    """(pointer, row stride) of a codes tensor."""
-    import torch
-    ld = _strided(t, name, (torch.float8_e4m3fn,))
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {(rows, cols)}")
-    if rows <= 1 or cols == 0:
-        ld = (cols + 15) // 16 * 16
-    if ld % 16 or t.data_ptr() % 16:
-        raise ValueError(f"{name} must have rows that start on 16 bytes (a row stride that is a multiple of 16)")
-    return t.data_ptr(), ld
-
-
-def _new_scales(rows, cols, device):
-    import torch
+def _new_scales(torch, rows, cols, device):
     k, t = (cols + 511) // 512, (rows + 127) // 128
     return torch.empty_strided((k, t, 512), (t * 512, 512, 1), dtype=torch.uint8, device=device)
-
-
-def _new_row_values(rows, device):
-    import torch
-    return torch.empty_strided((rows,), (1,), dtype=torch.float32, device=device)
-
-
-def _float_types():
-    import torch
-    return torch.bfloat16, torch.float32
 
 
 def tsenor_quantize(X, block: str = "row", mask=None, out=None, stream=None):
@@ -432,44 +400,57 @@ def tsenor_quantize(X, block: str = "row", mask=None, out=None, stream=None):
     whose bit is 0 counts as 0.  out: a QuantizedMatrix to write into.
     """
     import torch
-    ldx = _strided(X, "X", _float_types())
-    if block not in BLOCKS:
+    rows, cols, ldx = _rows(X, "X", (torch.bfloat16, torch.float32))
+    code = BLOCKS.get(block)
+    if code is None:
         raise ValueError(f"block must be one of {', '.join(BLOCKS)}, got {block!r}")
-    if _needs_guard(X.device, stream):
-        with _on(X.device, stream):
-            return tsenor_quantize(X, block, mask, out)
-    rows, cols = X.shape
     device = X.device
-    mask_ptr = _mask_pointer(mask, rows, cols, device)
+    if stream is not None or torch._C._cuda_getDevice() != device.index:
+        with _on(device, stream):
+            return tsenor_quantize(X, block, mask, out)
+    mask_ptr = None
+    if mask is not None:
+        mask_ptr = _dense(mask, "mask", torch.int32, (rows, words_per_row(cols)), device)
+    along = down = None
     if out is None:
-        out = QuantizedMatrix(_new_codes(rows, cols, device),
-                              _new_scales(rows, cols, device) if block != "column" else None,
-                              _new_scales(cols, rows, device) if block != "row" else None)
-        values, ldv = out.values.data_ptr(), (cols + 15) // 16 * 16
+        values, ldv = _new_codes(torch, rows, cols, device), (cols + 15) // 16 * 16
+        scales = _new_scales(torch, rows, cols, device) if code != 1 else None
+        scales_t = _new_scales(torch, cols, rows, device) if code != 0 else None
+        out = QuantizedMatrix(values, scales, scales_t)
+        ptr = values.data_ptr()
+        along = scales.data_ptr() if code != 1 else None
+        down = scales_t.data_ptr() if code != 0 else None
     else:
-        values, ldv = _codes(out.values, "out.values", device, (rows, cols))
-        if block != "column":
-            _dense(out.scales, "out.scales", torch.uint8, scale_shape(rows, cols), device)
-        if block != "row":
-            _dense(out.scales_t, "out.scales_t", torch.uint8, scale_shape(cols, rows), device)
-    _launch(lib().tsenor_quantize, device, X.data_ptr(), _dtype_code(X), rows, cols, ldx, BLOCKS[block], mask_ptr,
-            values, ldv, out.scales.data_ptr() if block != "column" else None,
-            out.scales_t.data_ptr() if block != "row" else None)
+        orows, ocols, ldv, ptr = _codes(out.values, "out.values", (torch.float8_e4m3fn,), device)
+        if (orows, ocols) != (rows, cols):
+            raise ValueError(f"out.values must have shape {(rows, cols)}, got {(orows, ocols)}")
+        if code != 1:
+            along = _dense(out.scales, "out.scales", torch.uint8, scale_shape(rows, cols), device)
+        if code != 0:
+            down = _dense(out.scales_t, "out.scales_t", torch.uint8, scale_shape(cols, rows), device)
+    status = lib().tsenor_quantize(X.data_ptr(), X.dtype == torch.bfloat16, rows, cols, ldx, code, mask_ptr, ptr, ldv, along,
+                                   down, torch._C._cuda_getCurrentRawStream(device.index))
+    if status:
+        _check(status)
     return out
 
 
 def tsenor_quantize_pair(X, stream=None):
     """(tsenor_quantize(X, "row"), tsenor_quantize(X, "column")) from one read of X."""
-    ldx = _strided(X, "X", _float_types())
-    if _needs_guard(X.device, stream):
-        with _on(X.device, stream):
+    import torch
+    rows, cols, ldx = _rows(X, "X", (torch.bfloat16, torch.float32))
+    device = X.device
+    if stream is not None or torch._C._cuda_getDevice() != device.index:
+        with _on(device, stream):
             return tsenor_quantize_pair(X)
-    rows, cols = X.shape
-    q = QuantizedMatrix(_new_codes(rows, cols, X.device), _new_scales(rows, cols, X.device), None)
-    t = QuantizedMatrix(_new_codes(rows, cols, X.device), None, _new_scales(cols, rows, X.device))
+    q = QuantizedMatrix(_new_codes(torch, rows, cols, device), _new_scales(torch, rows, cols, device), None)
+    t = QuantizedMatrix(_new_codes(torch, rows, cols, device), None, _new_scales(torch, cols, rows, device))
     ldv = (cols + 15) // 16 * 16
-    _launch(lib().tsenor_quantize_pair, X.device, X.data_ptr(), _dtype_code(X), rows, cols, ldx, q.values.data_ptr(),
-            ldv, q.scales.data_ptr(), t.values.data_ptr(), ldv, t.scales_t.data_ptr())
+    status = lib().tsenor_quantize_pair(X.data_ptr(), X.dtype == torch.bfloat16, rows, cols, ldx, q[0].data_ptr(), ldv,
+                                        q[1].data_ptr(), t[0].data_ptr(), ldv, t[2].data_ptr(),
+                                        torch._C._cuda_getCurrentRawStream(device.index))
+    if status:
+        _check(status)
     return q, t
 
 
@@ -477,36 +458,38 @@ def tsenor_dequantize(Q, dtype=None, out=None, stream=None):
     """What a QuantizedMatrix stands for, in bfloat16 or float32 (default); by ``scales`` where it has them."""
     import torch
     device = Q.values.device
-    rows, cols = Q.shape
-    ldv = _strided(Q.values, "Q.values", (torch.float8_e4m3fn,))
-    if Q.scales is not None:
-        _dense(Q.scales, "Q.scales", torch.uint8, scale_shape(rows, cols), device)
-    elif Q.scales_t is not None:
-        _dense(Q.scales_t, "Q.scales_t", torch.uint8, scale_shape(cols, rows), device)
-    else:
-        raise ValueError("Q has no scales")
-    if _needs_guard(device, stream):
+    rows, cols, ldv = _rows(Q.values, "Q.values", (torch.float8_e4m3fn,))
+    if stream is not None or torch._C._cuda_getDevice() != device.index:
         with _on(device, stream):
             return tsenor_dequantize(Q, dtype, out)
-    out, ldo = _output(out, rows, cols, dtype or torch.float32, device)
-    scales = Q.scales if Q.scales is not None else Q.scales_t
-    _launch(lib().tsenor_dequantize, device, Q.values.data_ptr(), rows, cols, ldv, scales.data_ptr(),
-            int(Q.scales is None), out.data_ptr(), _dtype_code(out), ldo)
+    if Q.scales is not None:
+        scales = _dense(Q.scales, "Q.scales", torch.uint8, scale_shape(rows, cols), device)
+    elif Q.scales_t is not None:
+        scales = _dense(Q.scales_t, "Q.scales_t", torch.uint8, scale_shape(cols, rows), device)
+    else:
+        raise ValueError("Q has no scales")
+    out, ldo = _output(torch, out, rows, cols, dtype, torch.float32, device)
+    status = lib().tsenor_dequantize(Q.values.data_ptr(), rows, cols, ldv, scales, Q.scales is None, out.data_ptr(),
+                                     out.dtype == torch.bfloat16, ldo, torch._C._cuda_getCurrentRawStream(device.index))
+    if status:
+        _check(status)
     return out
 
 
-def _output(out, rows, cols, dtype, device):
+def _output(torch, out, rows, cols, dtype, default, device):
     """(out, row stride): a given output checked, or a new one."""
-    import torch
     if out is None:
-        if dtype not in _float_types():
+        dtype = dtype or default
+        if dtype != torch.bfloat16 and dtype != torch.float32:
             raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
         return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device), cols
-    ldo = _strided(out, "out", _float_types())
+    orows, ocols, ldo = _rows(out, "out", (torch.bfloat16, torch.float32))
     if out.device != device:
         raise ValueError(f"out must be on {device}")
-    if tuple(out.shape) != (rows, cols):
-        raise ValueError(f"out must have shape {(rows, cols)}, got {tuple(out.shape)}")
+    if (orows, ocols) != (rows, cols):
+        raise ValueError(f"out must have shape {(rows, cols)}, got {(orows, ocols)}")
+    if dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out is {out.dtype}, dtype {dtype}")
     return out, ldo
 
 
@@ -520,64 +503,61 @@ def tsenor_matmul(A, B, form: str = "nt", mask=None, dtype=None, out=None, strea
     as 0.  dtype: torch.bfloat16 (default) or torch.float32, that of ``out`` when it is given.
     """
     import torch
-    if form not in FORMS:
+    code = FORMS.get(form)
+    if code is None:
         raise ValueError(f"form must be one of {', '.join(FORMS)}, got {form!r}")
-    device = A.values.device
-    if not A.values.is_cuda:
-        raise ValueError("A must be on a CUDA device")
-    if _needs_guard(device, stream):
+    av, bv = A[0], B[0]
+    device = av.device
+    types = (torch.float8_e4m3fn,)
+    ra, ca, lda, a = _codes(av, "A.values", types, device)
+    if stream is not None or torch._C._cuda_getDevice() != device.index:
         with _on(device, stream):
             return tsenor_matmul(A, B, form, mask, dtype, out)
-    a, lda = _codes(A.values, "A.values", device)
-    b, ldb = _codes(B.values, "B.values", device)
-    (ra, ca), (rb, cb) = A.values.shape, B.values.shape
-    m, k = (ca, ra) if form == "tn" else (ra, ca)
-    n, kb = (rb, cb) if form == "nt" else (cb, rb)
+    rb, cb, ldb, b = _codes(bv, "B.values", types, device)
+    m, k, sa = (ca, ra, A[2]) if code == 2 else (ra, ca, A[1])
+    n, kb, sb = (rb, cb, B[1]) if code == 0 else (cb, rb, B[2])
     if k != kb:
         raise ValueError(f"the operands sum over {k} and {kb} entries")
-    sa, sb = (A.scales_t if form == "tn" else A.scales), (B.scales if form == "nt" else B.scales_t)
     if sa is None or sb is None:
-        raise ValueError(f'form "{form}" needs {"A.scales_t" if form == "tn" else "A.scales"} and '
-                         f'{"B.scales" if form == "nt" else "B.scales_t"}')
-    _dense(sa, "A's scales", torch.uint8, scale_shape(m, k), device)
-    _dense(sb, "B's scales", torch.uint8, scale_shape(n, k), device)
-    mask_ptr = _mask_pointer(mask, m, n, device)
-    if dtype is not None and out is not None and out.dtype != dtype:
-        raise TypeError(f"out is {out.dtype}, dtype {dtype}")
-    out, ldo = _output(out, m, n, dtype or torch.bfloat16, device)
-    _launch(lib().tsenor_matmul, device, FORMS[form], a, lda, sa.data_ptr(), b, ldb, sb.data_ptr(), m, n, k, mask_ptr,
-            out.data_ptr(), _dtype_code(out), ldo)
+        raise ValueError(f'form "{form}" needs {"A.scales_t" if code == 2 else "A.scales"} and '
+                         f'{"B.scales" if code == 0 else "B.scales_t"}')
+    k4 = (k + 511) // 512
+    sa = _dense(sa, "A's scales", torch.uint8, (k4, (m + 127) // 128, 512), device)
+    sb = _dense(sb, "B's scales", torch.uint8, (k4, (n + 127) // 128, 512), device)
+    mask_ptr = None
+    if mask is not None:
+        mask_ptr = _dense(mask, "mask", torch.int32, (m, words_per_row(n)), device)
+    out, ldo = _output(torch, out, m, n, dtype, torch.bfloat16, device)
+    status = lib().tsenor_matmul(code, a, lda, sa, b, ldb, sb, m, n, k, mask_ptr, out.data_ptr(), out.dtype == torch.bfloat16,
+                                 ldo, torch._C._cuda_getCurrentRawStream(device.index))
+    if status:
+        _check(status)
     return out
 
 
-def _distill_args(logits, index, top_logits, temperature, teacher_lse):
+def _distill_args(torch, logits, index, top_logits, temperature, teacher_lse):
     """The arguments the distillation calls share, checked."""
-    import torch
-    ld = _strided(logits, "logits", _float_types())
-    rows, vocab = logits.shape
-    if index.dim() != 2 or index.shape[0] != rows:
+    rows, vocab, ld = _rows(logits, "logits", (torch.bfloat16, torch.float32))
+    device = logits.device
+    if index.dim() != 2:
         raise ValueError(f"index must have shape ({rows}, top), got {tuple(index.shape)}")
     top = index.shape[1]
-    _dense(index, "index", torch.int32, (rows, top), logits.device)
-    _dense(top_logits, "top_logits", torch.float32, (rows, top), logits.device)
-    if teacher_lse is not None:
-        _dense(teacher_lse, "teacher_lse", torch.float32, (rows,), logits.device)
-    return (logits.data_ptr(), _dtype_code(logits), rows, vocab, ld, index.data_ptr(), top_logits.data_ptr(), top,
-            teacher_lse.data_ptr() if teacher_lse is not None else None, float(temperature))
+    return (logits.data_ptr(), logits.dtype == torch.bfloat16, rows, vocab, ld,
+            _dense(index, "index", torch.int32, (rows, top), device),
+            _dense(top_logits, "top_logits", torch.float32, (rows, top), device), top,
+            None if teacher_lse is None else _dense(teacher_lse, "teacher_lse", torch.float32, (rows,), device), temperature)
 
 
-def _distill_grad_args(logits, weight, grad):
-    import torch
-    rows, vocab = logits.shape
-    if weight is not None:
-        _dense(weight, "weight", torch.float32, (rows,), logits.device)
+def _distill_grad_args(torch, logits, weight, grad):
+    """(grad, its row stride, pointer of weight)."""
+    (rows, vocab), device = logits.shape, logits.device
+    weight = None if weight is None else _dense(weight, "weight", torch.float32, (rows,), device)
     if grad is None:
-        grad, ldg = torch.empty_strided((rows, vocab), (vocab, 1), dtype=logits.dtype, device=logits.device), vocab
-    else:
-        ldg = _strided(grad, "grad", (logits.dtype,))
-        if grad.shape != logits.shape or grad.device != logits.device:
-            raise ValueError(f"grad must have shape {tuple(logits.shape)} on {logits.device}")
-    return grad, (weight.data_ptr() if weight is not None else None), ldg
+        return torch.empty_strided((rows, vocab), (vocab, 1), dtype=logits.dtype, device=device), vocab, weight
+    grows, gcols, ldg = _rows(grad, "grad", (logits.dtype,))
+    if (grows, gcols) != (rows, vocab) or grad.device != device:
+        raise ValueError(f"grad must have shape {(rows, vocab)} on {device}")
+    return grad, ldg, weight
 
 
 def tsenor_distill_loss(logits, index, top_logits, temperature: float = 1.0, teacher_lse=None, stream=None):
@@ -589,12 +569,19 @@ def tsenor_distill_loss(logits, index, top_logits, temperature: float = 1.0, tea
     softmax of top_logits / T over the row's entries, or, with teacher_lse (rows,)
     float32, exp(top_logits / T - teacher_lse).  lse is what tsenor_distill_grad takes.
     """
-    if logits.is_cuda and _needs_guard(logits.device, stream):
-        with _on(logits.device, stream):
+    import torch
+    args = _distill_args(torch, logits, index, top_logits, temperature, teacher_lse)
+    device = logits.device
+    if stream is not None or torch._C._cuda_getDevice() != device.index:
+        with _on(device, stream):
             return tsenor_distill_loss(logits, index, top_logits, temperature, teacher_lse)
-    args = _distill_args(logits, index, top_logits, temperature, teacher_lse)
-    loss, lse = _new_row_values(logits.shape[0], logits.device), _new_row_values(logits.shape[0], logits.device)
-    _launch(lib().tsenor_distill_loss, logits.device, *args, loss.data_ptr(), lse.data_ptr())
+    rows = args[2]
+    loss = torch.empty_strided((rows,), (1,), dtype=torch.float32, device=device)
+    lse = torch.empty_strided((rows,), (1,), dtype=torch.float32, device=device)
+    status = lib().tsenor_distill_loss(*args, loss.data_ptr(), lse.data_ptr(),
+                                       torch._C._cuda_getCurrentRawStream(device.index))
+    if status:
+        _check(status)
     return loss, lse
 
 
@@ -605,13 +592,18 @@ def tsenor_distill_step(logits, index, top_logits, temperature: float = 1.0, tea
     weight: (rows,) float32, default 1: the upstream gradient of each row's loss.
     grad: optional output like the logits, which may be the logits themselves.
     """
-    if logits.is_cuda and _needs_guard(logits.device, stream):
-        with _on(logits.device, stream):
+    import torch
+    args = _distill_args(torch, logits, index, top_logits, temperature, teacher_lse)
+    device = logits.device
+    if stream is not None or torch._C._cuda_getDevice() != device.index:
+        with _on(device, stream):
             return tsenor_distill_step(logits, index, top_logits, temperature, teacher_lse, weight, grad)
-    args = _distill_args(logits, index, top_logits, temperature, teacher_lse)
-    grad, weight_ptr, ldg = _distill_grad_args(logits, weight, grad)
-    loss = _new_row_values(logits.shape[0], logits.device)
-    _launch(lib().tsenor_distill_step, logits.device, *args, weight_ptr, loss.data_ptr(), grad.data_ptr(), ldg)
+    grad, ldg, weight_ptr = _distill_grad_args(torch, logits, weight, grad)
+    loss = torch.empty_strided((args[2],), (1,), dtype=torch.float32, device=device)
+    status = lib().tsenor_distill_step(*args, weight_ptr, loss.data_ptr(), grad.data_ptr(), ldg,
+                                       torch._C._cuda_getCurrentRawStream(device.index))
+    if status:
+        _check(status)
     return loss, grad
 
 
@@ -619,13 +611,17 @@ def tsenor_distill_grad(logits, index, top_logits, lse, temperature: float = 1.0
                         grad=None, stream=None):
     """weight * d loss / d logits, by the lse that tsenor_distill_loss gave for these logits; returns grad."""
     import torch
-    if logits.is_cuda and _needs_guard(logits.device, stream):
-        with _on(logits.device, stream):
+    args = _distill_args(torch, logits, index, top_logits, temperature, teacher_lse)
+    device = logits.device
+    if stream is not None or torch._C._cuda_getDevice() != device.index:
+        with _on(device, stream):
             return tsenor_distill_grad(logits, index, top_logits, lse, temperature, teacher_lse, weight, grad)
-    args = _distill_args(logits, index, top_logits, temperature, teacher_lse)
-    _dense(lse, "lse", torch.float32, (logits.shape[0],), logits.device)
-    grad, weight_ptr, ldg = _distill_grad_args(logits, weight, grad)
-    _launch(lib().tsenor_distill_grad, logits.device, *args, lse.data_ptr(), weight_ptr, grad.data_ptr(), ldg)
+    lse_ptr = _dense(lse, "lse", torch.float32, (args[2],), device)
+    grad, ldg, weight_ptr = _distill_grad_args(torch, logits, weight, grad)
+    status = lib().tsenor_distill_grad(*args, lse_ptr, weight_ptr, grad.data_ptr(), ldg,
+                                       torch._C._cuda_getCurrentRawStream(device.index))
+    if status:
+        _check(status)
     return grad
 
 
