@@ -114,15 +114,15 @@ struct Slice {
     }
 };
 
-// N threads of a block, from thread FIRST on, that meet at the block's barrier 1.
-template <int FIRST, int N>
+// N threads of a block, from thread FIRST on, that meet at the block's barrier ID.
+template <int FIRST, int N, int ID>
 struct Team {
     __device__ static int id() { return int(threadIdx.x) - FIRST; }
-    __device__ static void sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
+    __device__ static void sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory"); }
     __device__ static bool any(bool x) {
         uint32_t r;
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\tbar.red.or.pred p, 1, %2, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-                     : "=r"(r) : "r"(uint32_t(x)), "n"(N) : "memory");
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\tbar.red.or.pred p, %2, %3, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+                     : "=r"(r) : "r"(uint32_t(x)), "n"(ID), "n"(N) : "memory");
         return r != 0;
     }
     // In a fixed order; the result in every thread.  `red`: N / 32 values that may be used again after the next call.
@@ -154,12 +154,14 @@ struct Teacher {
     float* p;
     int* index;                                  // 16-byte aligned; -1: no entry
     int* table;                                  // of the indices seen, open addressing; `slots` a power of two
+    float* logit;                                // the student's logits of the entries' columns
 
     __device__ Teacher(void* at, int top_, int slots_) : top(top_), top4((top_ + 3) / 4 * 4), slots(slots_) {
         logp = static_cast<float*>(at);
         p = logp + top4;
         index = reinterpret_cast<int*>(p + top4);
         table = index + top4;
+        logit = reinterpret_cast<float*>(table + slots);
     }
 
     // Reads the entries; empty: none has weight, bad: the row fails.
@@ -183,8 +185,8 @@ struct Teacher {
         for (int j = TEAM::id(); j < top; j += N) {
             const int v = index[j];
             if (v < 0) continue;
-            for (unsigned h = first_slot(v);; ++h) {                         // half of the slots stay free
-                int* slot = table + (h & (slots - 1));
+            for (int k = 0; k < slots; ++k) {                                // half of the slots stay free
+                int* slot = table + ((first_slot(v) + k) & (slots - 1));
                 const int was = atomicCAS(slot, -1, v);
                 if (was == -1) break;
                 if ((was & ~kTwin) == v) {
@@ -195,9 +197,11 @@ struct Teacher {
         }
     }
     __device__ bool has_twin(int v) const {
-        unsigned h = first_slot(v);
-        while ((table[h & (slots - 1)] & ~kTwin) != v) ++h;
-        return table[h & (slots - 1)] & kTwin;
+        for (int k = 0; k < slots; ++k) {
+            const int was = table[(first_slot(v) + k) & (slots - 1)];
+            if ((was & ~kTwin) == v) return was & kTwin;
+        }
+        return false;
     }
     static constexpr int kTwin = 1 << 30;        // above every column
     __device__ static unsigned first_slot(int v) { return (unsigned(v) * 2654435761u) >> 7; }
@@ -250,7 +254,7 @@ int slots_of(int top) {
     while (n < 2 * top) n *= 2;
     return n;
 }
-unsigned teacher_bytes(int top) { return unsigned((top + 3) / 4 * 4 * 12 + slots_of(top) * 4); }
+unsigned teacher_bytes(int top) { return unsigned((top + 3) / 4 * 4 * 16 + slots_of(top) * 4); }
 
 // Gradient 0 for the columns of a slice.
 template <typename T, int M>
@@ -358,6 +362,22 @@ __device__ __forceinline__ Norm warp_join(Norm norm, float scale2) {
     return Norm{high, norm.sum};
 }
 
+// This slice's part of sum_j p_j (log p_j - z_j / T), and the entries' logits, by the threads of a team.
+template <typename T, typename TEAM, int N>
+__device__ double team_term(const DistillArgs& a, const typename T::storage* z, const Slice<T>& slice,
+                            const Teacher<TEAM, N>& teacher, double* red) {
+    double term = 0.0;
+    for (int j = TEAM::id(); j < a.top; j += N) {
+        const int v = teacher.index[j];
+        const float w = teacher.p[j];
+        if (v < 0 || !slice.has(v)) continue;
+        const float x = read<T>(z + v);
+        teacher.logit[j] = x;
+        if (w > 0.f) term += double(w) * (double(teacher.logp[j]) - double(x) * a.inv_t);
+    }
+    return TEAM::reduce(term, red, Plus());
+}
+
 // What a slice tells the others of its row.
 struct Share {
     Norm norm;
@@ -375,171 +395,202 @@ __device__ void write_loss(const DistillArgs& a, int64_t row, Norm norm, double 
     if (failed) atomicAdd(&g_row_failures, 1ull);
 }
 
-// Loss (STEP: and gradient).  A cluster of `slices` CTAs to a row.  Eight warps work on
-// the slice; four more start its copy and see to the teacher's entries meanwhile.
+// Loss (STEP: and gradient).  A cluster of `slices` CTAs walks the rows, one slice to a CTA.
+// Eight warps work on the slice in shared memory.  Four more are a row ahead: they see to the teacher's entries
+// and start the copy of each segment as soon as the workers have written the gradient of the one that it
+// replaces, so that reading, arithmetic and writing overlap within a CTA too.
+//   full[s]   segment s of this row is there          free[s]  its workers are done with it
+//   told[b]   the entries of a row (two buffers)      done[b]  its workers are done with them
+//   joined[b] the shares of all slices of the row
+// 2048 x 131072 bf16: TODO
 template <typename T, bool STEP>
 __global__ void __launch_bounds__(kThreads + kTeachers, 3)
-loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const int slots) {
+loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const int slots, const int teacher_room) {
     extern __shared__ __align__(128) uint4 chunk[];
-    __shared__ Share share[kMaxSlices];
-    __shared__ Norm part[kWarps];
-    __shared__ double term_of_slice;
-    __shared__ float extra[2 * Slice<T>::kPer];
-    __shared__ float total_of_p;
-    __shared__ int flags;                        // 1: no entry, 2: the row fails
-    __shared__ uint64_t bar[kMaxSegments];
-    __shared__ float red[3 * kTeachers / 32];
-    __shared__ double red64[kTeachers / 32];
     constexpr int kPer = Slice<T>::kPer;
+    __shared__ Share share[2][kMaxSlices];
+    __shared__ Norm part[2][kWarps];
+    __shared__ double red64[kTeachers / 32], term_of_slice[2];
+    __shared__ float red[3 * kTeachers / 32], total_of_p[2], extra[2][2 * kPer];
+    __shared__ int flags[2];                     // 1: no entry, 2: the row fails
+    __shared__ uint64_t full[kMaxSegments], free[kMaxSegments], told[2], done[2], joined[2];
+    using Extra = Team<kThreads, kTeachers, 1>;
+    using Workers = Team<0, kThreads, 2>;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int64_t row = blockIdx.x / unsigned(slices);
     const int rank = slices > 1 ? int(cluster_rank()) : 0;
-    const auto* z = static_cast<const typename T::storage*>(a.logits) + row * a.ld;
-    auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
-    const Slice<T> slice(z, int(a.vocab), rank, slices);
-    using Extra = Team<kThreads, kTeachers>;
-    Teacher<Extra, kTeachers> teacher(chunk + chunk_room, a.top, slots);
-    const bool vec = STEP && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
-    if (slices > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");      // every CTA of the row has begun
-    let_next_start();
-    prior_done();
-    if (t < slice.extras()) extra[t] = read<T>(z + slice.extra(t));
-    if (t == kThreads) {
-        for (int i = 0; i < kMaxSegments; ++i) mbar_init(bar + i, 1);
+    const int64_t first = blockIdx.x / unsigned(slices), step = gridDim.x / unsigned(slices);
+    const int segments = (chunk_room + kSegment - 1) / kSegment;
+    const float inv_t = 1.f / a.temperature, scale2 = inv_t * kLog2E;
+    if (t == 0) {
+        for (int i = 0; i < segments; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(free + i, kWarps);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(told + b, kTeachers / 32);
+            mbar_init(done + b, kWarps);
+            mbar_init(joined + b, slices);
+        }
         mbar_init_fence();
     }
-    __syncthreads();
-
-    const int segments = (slice.chunks + kSegment - 1) / kSegment;
-    const int early = STEP ? (segments + 1) / 2 : kMaxSegments;               // segments copied at once
-    auto logit_at = [&](int v) {
-        if (v < slice.head) return extra[v];
-        if (v >= slice.first && v < slice.first + slice.chunks * kPer)
-            return read<T>(reinterpret_cast<const typename T::storage*>(chunk) + (v - slice.first));
-        return extra[slice.head + v - (slice.vocab - slice.tail)];
+    let_next_start();
+    if (slices > 1) cluster_sync();              // peers write here
+    else __syncthreads();
+    prior_done();
+    auto row_of = [&](int64_t row) { return static_cast<const typename T::storage*>(a.logits) + row * a.ld; };
+    auto teacher_of = [&](int b) {
+        return Teacher<Extra, kTeachers>(reinterpret_cast<uint8_t*>(chunk + chunk_room) + b * teacher_room, a.top, slots);
     };
-    const float inv_t = 1.f / a.temperature, scale2 = inv_t * kLog2E;
-    const float2 by2 = make_float2(scale2, scale2);
     bool stalled = false;
+
     if (warp >= kWarps) {
-        bool empty, bad;
-        // Segments [from, to); those past the slice complete at once, as all do without bytes.
-        auto start_copy = [&](int from, int to, bool bytes) {
-            if (t != kThreads) return;
-            for (int i = from; i < to; ++i) {
-                const int c = i * kSegment, left = slice.chunks - c;
-                const int n = !bytes || left < 0 ? 0 : left < kSegment ? left : kSegment;
-                mbar_arrive_expect_tx(bar + i, n * 16);
-                if (n > 0) bulk_load(chunk + c, z + slice.first + c * kPer, n * 16, bar + i);
-            }
-        };
-        // half of a slice is on its way before it is known whether the row has entries
-        start_copy(0, early, true);
-        teacher.read_entries(a, row, &empty, &bad);
-        if (t == kThreads) flags = (empty ? 1 : 0) | (bad ? 2 : 0);
-        if (STEP) start_copy(early, kMaxSegments, !empty && !bad);
-        if (!empty && !(STEP && bad)) {
-            if (STEP) teacher.mark_twins();
-            const float total = teacher.weights(a, row, red);
-            for (int i = 0; i < segments; ++i)
-                if (!mbar_sleep_bounded(bar + i, 0)) stalled = true;
-            // sum_j p_j (log p_j - z_j / T) of the entries in this slice
-            double term = 0.0;
-            for (int j = Extra::id(); j < a.top; j += kTeachers) {
-                const int v = teacher.index[j];
-                const float w = teacher.p[j];
-                if (v >= 0 && w > 0.f && slice.has(v))
-                    term += double(w) * (double(teacher.logp[j]) - double(logit_at(v)) * a.inv_t);
-            }
-            term = Extra::reduce(term, red64, Plus());
-            if (t == kThreads) {
-                total_of_p = total;
-                term_of_slice = term;
-            }
-        }
-    } else {
-        // one pass over the slice; a NaN or +inf anywhere makes the sum NaN
-        Norm norm{-INFINITY, 0.f};
-        for (int i = 0; i < segments; ++i) {
-            if (!mbar_sleep_bounded(bar + i, 0)) stalled = true;
-            if (STEP && i >= early && flags) break;          // written before segment `early` began
-            const uint4* from = chunk + i * kSegment + t;
-            const int left = slice.chunks - i * kSegment - t;
-            if (left > (kGroup - 1) * kThreads) {
-                uint4 v[kGroup];
-#pragma unroll
-                for (int k = 0; k < kGroup; ++k) v[k] = from[k * kThreads];
-                take<T, kGroup>(norm, v, scale2);
-            } else {
-                for (int k = 0; k * kThreads < left; ++k) {
-                    const uint4 v = from[k * kThreads];
-                    take<T, 1>(norm, &v, scale2);
+        unsigned i = 0;
+        for (int64_t row = first; row < a.rows; row += step, ++i) {
+            const int b = i & 1;
+            const auto* z = row_of(row);
+            const Slice<T> slice(z, int(a.vocab), rank, slices);
+            Teacher<Extra, kTeachers> teacher = teacher_of(b);
+            if (i > 1 && !mbar_sleep_bounded(done + b, ((i >> 1) - 1) & 1)) { stalled = true; break; }
+            bool empty, bad;
+            teacher.read_entries(a, row, &empty, &bad);
+            if (t == kThreads) flags[b] = (empty ? 1 : 0) | (bad ? 2 : 0);
+            const bool skip = STEP && (empty || bad);                         // the logits are not read
+            // segments past the slice complete at once, as all do without bytes
+            auto copy = [&](int s) {
+                const int c = s * kSegment, left = slice.chunks - c;
+                const int n = skip || left < 0 ? 0 : left < kSegment ? left : kSegment;
+                mbar_arrive_expect_tx(full + s, n * 16);
+                if (n > 0) bulk_load(chunk + c, z + slice.first + c * kPer, n * 16, full + s);
+            };
+            if (i == 0 && t == kThreads)
+                for (int s = 0; s < segments; ++s) copy(s);
+            const int e = t - kThreads;
+            if (e < slice.extras()) extra[b][e] = read<T>(z + slice.extra(e));
+            if (!empty && !(STEP && bad)) {
+                if (STEP) teacher.mark_twins();
+                const float total = teacher.weights(a, row, red);
+                const double term = team_term<T, Extra, kTeachers>(a, z, slice, teacher, red64);
+                if (t == kThreads) {
+                    total_of_p[b] = total;
+                    term_of_slice[b] = term;
                 }
             }
-        }
-        if (t < slice.extras()) take_one(norm, extra[t], scale2);
-        if (stalled) norm.sum = NAN;
-        norm = warp_join(norm, scale2);
-        if (lane == 0) part[warp] = norm;
-    }
-    __syncthreads();
-    const bool empty = flags & 1;
-    bool failed = flags & 2;
-    if (STEP && flags) {
-        if (slices > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-        if (warp < kWarps) write_zeros<T, kThreads>(g, slice, vec);
-        if (t == 0 && rank == 0) {
-            a.loss[row] = failed ? NAN : 0.f;
-            if (failed) atomicAdd(&g_row_failures, 1ull);
-        }
-        return;
-    }
-
-    Norm norm = join(kWarps, scale2, [&](int k) { return part[k]; });
-    double term = term_of_slice;
-    if (slices > 1) {
-        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-        if (warp == 0) {
-            if (t < slices) {
-                const uint32_t to = cluster_addr(smem_u32(share + rank), t);
-                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(norm.high), "f"(norm.sum) : "memory");
-                asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to + 8), "d"(term) : "memory");
-            }
             __syncwarp();
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        } else {
-            asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+            if (lane == 0) mbar_arrive(told + b);
+            if (i > 0 && warp == kWarps) {
+                for (int s = 0; s < segments && !stalled; ++s) {
+                    if (!mbar_sleep_bounded(free + s, (i - 1) & 1)) stalled = true;
+                    else if (lane == 0) copy(s);
+                    __syncwarp();
+                }
+            }
+            if (Extra::any(stalled)) { stalled = true; break; }
         }
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        norm = join(slices, scale2, [&](int k) { return share[k].norm; });
-        term = 0.0;
-        for (int k = 0; k < slices; ++k) term += share[k].term;
-    }
-    const float m = norm.high;
-    failed = failed || (!empty && !(fabsf(m) < INFINITY && norm.sum < INFINITY));
-    if (t == kThreads && rank == 0) write_loss<STEP>(a, row, norm, term, total_of_p, empty, failed);
-    if constexpr (STEP) {
-        const float by = a.temperature * (a.weight ? a.weight[row] : 1.f);
-        if (failed || by == 0.f) {
-            if (warp < kWarps) write_zeros<T, kThreads>(g, slice, vec);
-            return;
-        }
-        const float scale = by * total_of_p / norm.sum;
-        auto at = [&](float x) { return scale * ex2((x - m) * scale2); };
-        if (warp < kWarps) {
-            const float2 minus_m = make_float2(-m, -m), scale_2 = make_float2(scale, scale);
+        // copies in flight end before the block does
+        if (stalled && warp == kWarps)
+            for (int s = 0; s < segments; ++s) mbar_sleep_bounded(full + s, i & 1);
+    } else {
+        unsigned i = 0, joins = 0;
+        for (int64_t row = first; row < a.rows; row += step, ++i) {
+            const int b = i & 1;
+            const auto* z = row_of(row);
+            auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
+            const Slice<T> slice(z, int(a.vocab), rank, slices);
+            const bool vec = STEP && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+            auto leave = [&](uint64_t* bar) {    // this warp is done with what the barrier stands for
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar);
+            };
+            // one pass over the slice; a NaN or +inf anywhere makes the sum NaN
+            Norm norm{-INFINITY, 0.f};
+            for (int s = 0; s < segments; ++s) {
+                if (!mbar_sleep_bounded(full + s, i & 1)) { stalled = true; break; }
+                if (STEP && flags[b]) break;     // written before the first segment began
+                const uint4* from = chunk + s * kSegment + t;
+                const int left = slice.chunks - s * kSegment - t;
+                if (left > (kGroup - 1) * kThreads) {
+                    uint4 v[kGroup];
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k) v[k] = from[k * kThreads];
+                    take<T, kGroup>(norm, v, scale2);
+                } else {
+                    for (int k = 0; k * kThreads < left; ++k) {
+                        const uint4 v = from[k * kThreads];
+                        take<T, 1>(norm, &v, scale2);
+                    }
+                }
+                if (!STEP) leave(free + s);
+            }
+            if (!mbar_sleep_bounded(told + b, (i >> 1) & 1)) stalled = true;
+            if (Workers::any(stalled)) { stalled = true; break; }
+            const bool empty = flags[b] & 1;
+            bool failed = flags[b] & 2;
+            Teacher<Extra, kTeachers> teacher = teacher_of(b);
+            if (STEP && flags[b]) {
+                for (int s = 0; s < segments; ++s) leave(free + s);
+                write_zeros<T, kThreads>(g, slice, vec);
+                if (t == 0 && rank == 0) {
+                    a.loss[row] = failed ? NAN : 0.f;
+                    if (failed) atomicAdd(&g_row_failures, 1ull);
+                }
+                leave(done + b);
+                continue;
+            }
+            if (t < slice.extras()) take_one(norm, extra[b][t], scale2);
+            norm = warp_join(norm, scale2);
+            if (lane == 0) part[b][warp] = norm;
+            Workers::sync();
+            norm = join(kWarps, scale2, [&](int k) { return part[b][k]; });
+            double term = empty ? 0.0 : term_of_slice[b];
+            const float total = empty ? 0.f : total_of_p[b];
+            if (slices > 1) {
+                const int j = joins & 1;
+                if (t < slices) {
+                    const uint32_t to = cluster_addr(smem_u32(&share[j][rank]), t);
+                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(norm.high), "f"(norm.sum) : "memory");
+                    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to + 8), "d"(term) : "memory");
+                    cluster_arrive(cluster_addr(smem_u32(joined + j), t));
+                }
+                if (!mbar_cluster_sleep_bounded(joined + j, (joins >> 1) & 1)) stalled = true;
+                if (Workers::any(stalled)) { stalled = true; break; }
+                ++joins;
+                norm = join(slices, scale2, [&](int k) { return share[j][k].norm; });
+                term = 0.0;
+                for (int k = 0; k < slices; ++k) term += share[j][k].term;
+            }
+            const float m = norm.high;
+            failed = failed || (!empty && !(fabsf(m) < INFINITY && norm.sum < INFINITY));
+            if (t == 0 && rank == 0) write_loss<STEP>(a, row, norm, term, total, empty, failed);
+            if constexpr (STEP) {
+                const float by = a.temperature * (a.weight ? a.weight[row] : 1.f);
+                if (failed || by == 0.f) {
+                    for (int s = 0; s < segments; ++s) leave(free + s);
+                    write_zeros<T, kThreads>(g, slice, vec);
+                } else {
+                    const float scale = by * total / norm.sum;
+                    auto at = [&](float x) { return scale * ex2((x - m) * scale2); };
+                    const float2 minus_m = make_float2(-m, -m), scale_2 = make_float2(scale, scale),
+                                 by2 = make_float2(scale2, scale2);
+                    for (int s = 0; s < segments; ++s) {
+                        const int end = slice.chunks < (s + 1) * kSegment ? slice.chunks : (s + 1) * kSegment;
 #pragma unroll 4
-            for (int c = t; c < slice.chunks; c += kThreads)
-                write_chunk<T>(g + slice.first + c * kPer, chunk[c], vec, [&](float2 x) {
-                    x = mul2(add2(x, minus_m), by2);
-                    return mul2(make_float2(ex2(x.x), ex2(x.y)), scale_2);
-                });
-            if (t < slice.extras()) write<T>(g + slice.extra(t), at(extra[t]));
+                        for (int c = s * kSegment + t; c < end; c += kThreads)
+                            write_chunk<T>(g + slice.first + c * kPer, chunk[c], vec, [&](float2 x) {
+                                x = mul2(add2(x, minus_m), by2);
+                                return mul2(make_float2(ex2(x.x), ex2(x.y)), scale_2);
+                            });
+                        leave(free + s);
+                    }
+                    if (t < slice.extras()) write<T>(g + slice.extra(t), at(extra[b][t]));
+                    Workers::sync();             // the entries' columns are written again
+                    teacher.template each<kThreads>(slice, [&](int j, int v, float w) { write<T>(g + v, at(teacher.logit[j]) - by * w); });
+                }
+            }
+            leave(done + b);
         }
-        __syncthreads();                         // the entries' columns are written again
-        if (warp < kWarps)
-            teacher.template each<kThreads>(slice, [&](int, int v, float w) { write<T>(g + v, at(logit_at(v)) - by * w); });
     }
+    if (stalled && lane == 0) atomicAdd(&g_row_failures, 1ull);
+    if (slices > 1) cluster_sync();              // no peer writes here any more
 }
 
 // The same with one CTA to a row, which streams it through registers, twice for the step
@@ -559,9 +610,8 @@ stream_kernel(const DistillArgs a, const int slots) {
     const auto* z = static_cast<const typename T::storage*>(a.logits) + row * a.ld;
     auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
     const Slice<T> slice(z, int(a.vocab), 0, 1);
-    using Extra = Team<kThreads, kTeachers>;
+    using Extra = Team<kThreads, kTeachers, 1>;
     Teacher<Extra, kTeachers> teacher(room, a.top, slots);
-    float* logit = reinterpret_cast<float*>(teacher.table + slots);      // of the entries' columns
     const bool vec = STEP && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     const float inv_t = 1.f / a.temperature, scale2 = inv_t * kLog2E;
     const uint4* in = reinterpret_cast<const uint4*>(z + slice.first);
@@ -575,17 +625,7 @@ stream_kernel(const DistillArgs a, const int slots) {
         if (!empty && !(STEP && bad)) {
             if (STEP) teacher.mark_twins();
             const float total = teacher.weights(a, row, red);
-            // sum_j p_j (log p_j - z_j / T)
-            double term = 0.0;
-            for (int j = Extra::id(); j < a.top; j += kTeachers) {
-                const int v = teacher.index[j];
-                const float w = teacher.p[j];
-                if (v < 0) continue;
-                const float x = read<T>(z + v);
-                logit[j] = x;
-                if (w > 0.f) term += double(w) * (double(teacher.logp[j]) - double(x) * a.inv_t);
-            }
-            term = Extra::reduce(term, red64, Plus());
+            const double term = team_term<T, Extra, kTeachers>(a, z, slice, teacher, red64);
             if (t == kThreads) {
                 total_of_p = total;
                 term_of_row = term;
@@ -655,7 +695,7 @@ stream_kernel(const DistillArgs a, const int slots) {
         }
         __syncthreads();                         // the entries' columns are written again
         if (warp < kWarps)
-            teacher.template each<kThreads>(slice, [&](int j, int v, float w) { write<T>(g + v, at(logit[j]) - by * w); });
+            teacher.template each<kThreads>(slice, [&](int j, int v, float w) { write<T>(g + v, at(teacher.logit[j]) - by * w); });
     }
 }
 
@@ -672,7 +712,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     const auto* z = static_cast<const typename T::storage*>(a.logits) + row * a.ld;
     auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
     const Slice<T> slice(z, int(a.vocab), rank, slices);
-    Teacher<Team<0, kThreads>, kThreads> teacher(room, a.top, slots);
+    Teacher<Team<0, kThreads, 1>, kThreads> teacher(room, a.top, slots);
     float* target = teacher.logp;                // log p is not needed here
     const bool vec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     let_next_start();
@@ -738,16 +778,24 @@ template <typename T, bool STEP>
 cudaError_t launch_loss(const DistillArgs& a, cudaStream_t st) {
     const int64_t row_bytes = a.vocab * int64_t(sizeof(typename T::storage));
     if (streams(STEP, a.rows, row_bytes)) {
-        return launch_early(stream_kernel<T, STEP>, a.rows, kThreads + kTeachers, teacher_bytes(a.top) + a.top * 4, 1, st, a,
+        return launch_early(stream_kernel<T, STEP>, a.rows, kThreads + kTeachers, teacher_bytes(a.top), 1, st, a,
                             slots_of(a.top));
     }
     const int slices = slices_of(a.rows, row_bytes);
     const int chunk_room = int((row_bytes / 16 + slices - 1) / slices);
-    const unsigned bytes = unsigned(chunk_room * 16) + teacher_bytes(a.top);
+    const unsigned teacher_room = (teacher_bytes(a.top) + 15) / 16 * 16, bytes = unsigned(chunk_room * 16) + 2 * teacher_room;
     cudaError_t e = cudaFuncSetAttribute(loss_kernel<T, STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
-    return launch_early(loss_kernel<T, STEP>, a.rows * slices, kThreads + kTeachers, bytes, slices, st, a, slices, chunk_room,
-                        slots_of(a.top));
+    // No more clusters than run at once, or the last ones would start when the others are through.
+    int64_t clusters = a.rows;
+    if (clusters * slices > 148) {
+        int fit = 0;
+        e = clusters_that_fit(&fit, loss_kernel<T, STEP>, kThreads + kTeachers, bytes, slices);
+        if (e != cudaSuccess) return e;
+        if (fit > 0 && clusters > fit) clusters = fit;
+    }
+    return launch_early(loss_kernel<T, STEP>, clusters * slices, kThreads + kTeachers, bytes, slices, st, a, slices, chunk_room,
+                        slots_of(a.top), int(teacher_room));
 }
 
 template <typename T>

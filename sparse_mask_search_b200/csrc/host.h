@@ -36,6 +36,22 @@ cudaError_t launch_early(void (*kernel)(P...), int64_t grid, int block, size_t s
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// How many clusters of a kernel the current device runs at once.
+template <typename... P>
+cudaError_t clusters_that_fit(int* count, void (*kernel)(P...), int block, size_t smem, int cluster) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(cluster));
+    cfg.blockDim = dim3(unsigned(block));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(count, kernel, &cfg);
+}
+
 // Adds the rows that failed in the distillation kernels on the current device
 // since the last call to *count and resets them (ordered on `st`).
 cudaError_t read_row_failures(cudaStream_t st, unsigned long long* count);

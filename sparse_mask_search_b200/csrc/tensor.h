@@ -143,6 +143,20 @@ __device__ __forceinline__ bool mbar_sleep_bounded(uint64_t* bar, unsigned parit
     return false;
 }
 
+// The same for a barrier on which other CTAs of the cluster arrive: what they wrote before is visible after it.
+__device__ __forceinline__ bool mbar_cluster_sleep_bounded(uint64_t* bar, unsigned parity) {
+    for (unsigned k = 0; k < kTmaPolls; ++k) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done) : "r"(smem_u32(bar)), "r"(parity), "r"(2000u) : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+
 // ---- copies and clusters ----------------------------------------------------------------
 
 // `bytes` (a multiple of 16, both ends 16-byte aligned) from global memory into this CTA.
