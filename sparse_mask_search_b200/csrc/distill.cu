@@ -226,10 +226,10 @@ struct Teacher {
         }
         return TEAM::reduce(total, red + 2 * (N / 32), Plus());
     }
-    // Threads 0 to M - 1: f(j, v, sum of the weights of index v) for the entries in a slice, each index once.
+    // Thread `me` of M: f(j, v, sum of the weights of index v) for the entries in a slice, each index once.
     template <int M, typename S, typename F>
-    __device__ __forceinline__ void each(const S& slice, F f) const {
-        for (int j = threadIdx.x; j < top; j += M) {
+    __device__ __forceinline__ void each(int me, const S& slice, F f) const {
+        for (int j = me; j < top; j += M) {
             const int v = index[j];
             if (v < 0 || !slice.has(v)) continue;
             bool first = true;
@@ -413,6 +413,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
     __shared__ double red64[kTeachers / 32], term_of_slice[2];
     __shared__ float red[3 * kTeachers / 32], total_of_p[2], extra[2][2 * kPer];
     __shared__ int flags[2];                     // 1: no entry, 2: the row fails
+    __shared__ float row_high[2], row_scale[2], row_by[2];                    // of a row's gradient; by 0: it is 0
     __shared__ uint64_t full[kMaxSegments], free[kMaxSegments], told[2], done[2], joined[2];
     using Extra = Team<kThreads, kTeachers, 1>;
     using Workers = Team<0, kThreads, 2>;
@@ -445,12 +446,25 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
 
     if (warp >= kWarps) {
         unsigned i = 0;
+        // the columns of a row's entries, once the workers have written the row (its number here: n)
+        auto write_targets = [&](int64_t row, unsigned n) {
+            const int b = n & 1;
+            if (!mbar_sleep_bounded(done + b, (n >> 1) & 1)) return false;
+            if (!STEP || row_by[b] == 0.f) return true;
+            const float scale = row_scale[b], m = row_high[b], by = row_by[b];
+            auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
+            const Slice<T> slice(row_of(row), int(a.vocab), rank, slices);
+            const Teacher<Extra, kTeachers> teacher = teacher_of(b);
+            teacher.template each<kTeachers>(Extra::id(), slice, [&](int j, int v, float w) {
+                write<T>(g + v, scale * ex2((teacher.logit[j] - m) * scale2) - by * w);
+            });
+            return true;
+        };
         for (int64_t row = first; row < a.rows; row += step, ++i) {
             const int b = i & 1;
             const auto* z = row_of(row);
             const Slice<T> slice(z, int(a.vocab), rank, slices);
             Teacher<Extra, kTeachers> teacher = teacher_of(b);
-            if (i > 1 && !mbar_sleep_bounded(done + b, ((i >> 1) - 1) & 1)) { stalled = true; break; }
             bool empty, bad;
             teacher.read_entries(a, row, &empty, &bad);
             if (t == kThreads) flags[b] = (empty ? 1 : 0) | (bad ? 2 : 0);
@@ -484,8 +498,10 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
                     __syncwarp();
                 }
             }
+            if (i > 0 && !write_targets(row - step, i - 1)) stalled = true;
             if (Extra::any(stalled)) { stalled = true; break; }
         }
+        if (STEP && i > 0 && !stalled && !write_targets(first + (i - 1) * step, i - 1)) stalled = true;
         // copies in flight end before the block does
         if (stalled && warp == kWarps)
             for (int s = 0; s < segments; ++s) mbar_sleep_bounded(full + s, i & 1);
@@ -525,7 +541,6 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
             if (Workers::any(stalled)) { stalled = true; break; }
             const bool empty = flags[b] & 1;
             bool failed = flags[b] & 2;
-            Teacher<Extra, kTeachers> teacher = teacher_of(b);
             if (STEP && flags[b]) {
                 for (int s = 0; s < segments; ++s) leave(free + s);
                 write_zeros<T, kThreads>(g, slice, vec);
@@ -533,6 +548,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
                     a.loss[row] = failed ? NAN : 0.f;
                     if (failed) atomicAdd(&g_row_failures, 1ull);
                 }
+                if (t == 0) row_by[b] = 0.f;
                 leave(done + b);
                 continue;
             }
@@ -568,7 +584,6 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
                     write_zeros<T, kThreads>(g, slice, vec);
                 } else {
                     const float scale = by * total / norm.sum;
-                    auto at = [&](float x) { return scale * ex2((x - m) * scale2); };
                     const float2 minus_m = make_float2(-m, -m), scale_2 = make_float2(scale, scale),
                                  by2 = make_float2(scale2, scale2);
                     for (int s = 0; s < segments; ++s) {
@@ -581,9 +596,12 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
                             });
                         leave(free + s);
                     }
-                    if (t < slice.extras()) write<T>(g + slice.extra(t), at(extra[b][t]));
-                    Workers::sync();             // the entries' columns are written again
-                    teacher.template each<kThreads>(slice, [&](int j, int v, float w) { write<T>(g + v, at(teacher.logit[j]) - by * w); });
+                    if (t < slice.extras()) write<T>(g + slice.extra(t), scale * ex2((extra[b][t] - m) * scale2));
+                }
+                if (t == 0) {
+                    row_high[b] = m;
+                    row_scale[b] = by * total / norm.sum;
+                    row_by[b] = failed ? 0.f : by;
                 }
             }
             leave(done + b);
@@ -695,7 +713,7 @@ stream_kernel(const DistillArgs a, const int slots) {
         }
         __syncthreads();                         // the entries' columns are written again
         if (warp < kWarps)
-            teacher.template each<kThreads>(slice, [&](int j, int v, float w) { write<T>(g + v, at(teacher.logit[j]) - by * w); });
+            teacher.template each<kThreads>(t, slice, [&](int j, int v, float w) { write<T>(g + v, at(teacher.logit[j]) - by * w); });
     }
 }
 
@@ -741,7 +759,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     const float inv_t = 1.f / a.temperature, scale = by * total;
     auto at = [&](float x) { return scale * ex2(fmaf(x, inv_t, -lse) * kLog2E); };
     // the entries' gradients before anything is written: grad may be the logits
-    teacher.template each<kThreads>(slice, [&](int j, int c, float w) { target[j] = at(read<T>(z + c)) - by * w; });
+    teacher.template each<kThreads>(t, slice, [&](int j, int c, float w) { target[j] = at(read<T>(z + c)) - by * w; });
     __syncthreads();
     const float2 inv2 = make_float2(inv_t, inv_t), minus = make_float2(-lse, -lse), l2 = make_float2(kLog2E, kLog2E),
                  scale_2 = make_float2(scale, scale);
@@ -757,7 +775,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     }
     if (t < slice.extras()) write<T>(g + slice.extra(t), at(read<T>(z + slice.extra(t))));
     __syncthreads();
-    teacher.template each<kThreads>(slice, [&](int j, int c, float) { write<T>(g + c, target[j]); });
+    teacher.template each<kThreads>(t, slice, [&](int j, int c, float) { write<T>(g + c, target[j]); });
 }
 
 // Slices of a row: at most kSliceBytes each, and for few rows enough CTAs to fill the
