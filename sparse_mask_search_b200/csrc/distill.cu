@@ -587,13 +587,23 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
                     const float2 minus_m = make_float2(-m, -m), scale_2 = make_float2(scale, scale),
                                  by2 = make_float2(scale2, scale2);
                     for (int s = 0; s < segments; ++s) {
-                        const int end = slice.chunks < (s + 1) * kSegment ? slice.chunks : (s + 1) * kSegment;
-#pragma unroll 4
-                        for (int c = s * kSegment + t; c < end; c += kThreads)
-                            write_chunk<T>(g + slice.first + c * kPer, chunk[c], vec, [&](float2 x) {
-                                x = mul2(add2(x, minus_m), by2);
-                                return mul2(make_float2(ex2(x.x), ex2(x.y)), scale_2);
-                            });
+                        auto gradient = [&](float2 x) {
+                            x = mul2(add2(x, minus_m), by2);
+                            return mul2(make_float2(ex2(x.x), ex2(x.y)), scale_2);
+                        };
+                        const uint4* from = chunk + s * kSegment + t;
+                        auto* to = g + slice.first + (s * kSegment + t) * kPer;
+                        const int left = slice.chunks - s * kSegment - t;
+                        if (left > (kGroup - 1) * kThreads) {
+                            uint4 v[kGroup];
+#pragma unroll
+                            for (int k = 0; k < kGroup; ++k) v[k] = from[k * kThreads];
+#pragma unroll
+                            for (int k = 0; k < kGroup; ++k) write_chunk<T>(to + k * kThreads * kPer, v[k], vec, gradient);
+                        } else {
+                            for (int k = 0; k * kThreads < left; ++k)
+                                write_chunk<T>(to + k * kThreads * kPer, from[k * kThreads], vec, gradient);
+                        }
                         leave(free + s);
                     }
                     if (t < slice.extras()) write<T>(g + slice.extra(t), scale * ex2((extra[b][t] - m) * scale2));
