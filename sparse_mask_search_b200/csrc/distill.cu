@@ -521,7 +521,9 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
             Norm norm{-INFINITY, 0.f};
             for (int s = 0; s < segments; ++s) {
                 if (!mbar_sleep_bounded(full + s, i & 1)) { stalled = true; break; }
-                if (STEP && flags[b]) break;     // written before the first segment began
+                // Written before the first segment began.  A row that is not read waits for its (empty) segments all the
+                // same: its arrivals on free[s] must not overtake the copying warp's wait on them.
+                if (STEP && flags[b]) continue;
                 const uint4* from = chunk + s * kSegment + t;
                 const int left = slice.chunks - s * kSegment - t;
                 if (left > (kGroup - 1) * kThreads) {

@@ -245,10 +245,11 @@ __global__ void __launch_bounds__(kQThreads, sizeof(typename T::storage) == 2 ? 
     let_next_start();
     prior_done();
     // A tile with all its columns loads 16 bytes at a time, all in flight together.  Where rows do
-    // not start on 16 bytes, the loads cover whole aligned words, which must not lie
-    // outside x: the first and the last tile go entry by entry, as do tiles that are cut.
+    // not start on 16 bytes, the loads cover whole aligned words, up to 15 bytes more on either side, which
+    // must not lie outside x: the first tile, and those of the last rows without 8 more columns behind
+    // them, go entry by entry, as do tiles that are cut.
     const bool whole = tc * 128 + 128 <= a.cols &&
-                       (VEC || (blockIdx.x > 0 && blockIdx.x + 1 < a.tiles_r * a.tiles_c));
+                       (VEC || (blockIdx.x > 0 && (tr + 1 < a.tiles_r || tc * 128 + 136 <= a.cols)));
     if (whole) {
 #pragma unroll
         for (int p = 0; p < kPass; ++p) {

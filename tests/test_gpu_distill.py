@@ -188,6 +188,57 @@ def test_strided_rows_and_the_gradient_in_place(dtype, rows, vocab):
         assert bool((buf[rest] == 5.0).all())
 
 
+@pytest.mark.parametrize("dtype,rows,vocab", [("bf16", 600, 33000), ("bf16", 450, 60001), ("f32", 120, 131072), ("f32", 150, 262143),
+                                              ("bf16", 700, 5003), ("bf16", 147, 200001)])
+@pytest.mark.parametrize("top", [9, 200])
+def test_many_rows_of_every_kind(dtype, rows, vocab, top):
+    # blocks that walk several rows: with and without entries, failing, without weight, in any order
+    z, index, value, _ = _case(rows, vocab, top, dtype, 11)
+    kind = torch.randint(0, 8, (rows,), generator=_gen(12), device="cuda")
+    index[kind == 0] = -1
+    weight = torch.rand((rows,), generator=_gen(13), device="cuda")
+    weight[kind == 1] = 0.0
+    index[kind == 2, top // 2:] = -1
+    loss, lse, grad, tol_loss, tol_grad = _reference(z, index, value, 2.0, None, weight)
+    bad = kind == 3
+    index[bad, 0] = vocab
+    z[bad & (torch.arange(rows, device="cuda") % 2 == 0), vocab // 2] = torch.nan
+    tsl.tsenor_error_count()
+    got, g = tsl.tsenor_distill_step(z, index, value, 2.0, weight=weight)
+    assert tsl.tsenor_error_count() == int(bad.sum())
+    assert bool(got[bad].isnan().all()) and bool((g[bad | (kind == 0) | (kind == 1)] == 0).all())
+    _near(got[~bad], loss[~bad], tol_loss[~bad])
+    tol_grad = tol_grad + torch.finfo(z.dtype).eps / 2 * grad.abs() + torch.finfo(z.dtype).tiny
+    _near(g[~bad], grad[~bad], tol_grad[~bad])
+    got2, lse2 = tsl.tsenor_distill_loss(z, index, value, 2.0)
+    _near(got2[~bad], loss[~bad], tol_loss[~bad])
+    _near(lse2[~bad], lse[~bad], 2.0 ** -24 * (4 * lse.abs() + vocab / 256 + 128)[~bad])
+    inner = z.clone()
+    got3, _ = tsl.tsenor_distill_step(inner, index, value, 2.0, weight=weight, grad=inner)
+    assert torch.equal(inner, g) and torch.equal(got3[~bad], got[~bad])
+    tsl.tsenor_error_count()
+
+
+@pytest.mark.parametrize("dtype,rows,vocab", [("bf16", 500, 33000), ("f32", 100, 131072)])
+def test_captured_and_replayed(dtype, rows, vocab):
+    first, second = (_case(rows, vocab, 20, dtype, s)[:3] for s in (14, 15))
+    want = []
+    for z, index, value in (first, second):
+        loss, lse = tsl.tsenor_distill_loss(z, index, value, 2.0)
+        want.append((loss, lse, *tsl.tsenor_distill_step(z, index, value, 2.0), tsl.tsenor_distill_grad(z, index, value, lse, 2.0)))
+    held = [t.clone() for t in first]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, lse = tsl.tsenor_distill_loss(*held, 2.0)
+        out = (loss, lse, *tsl.tsenor_distill_step(*held, 2.0), tsl.tsenor_distill_grad(*held, lse, 2.0))
+    for case, w in ((second, want[1]), (first, want[0]), (second, want[1])):
+        for h, t in zip(held, case):
+            h.copy_(t)
+        graph.replay()
+        for a, b in zip(out, w):
+            assert torch.equal(a, b)
+
+
 def test_gradient_against_differences():
     # loss in fp32 along a random direction: central differences of step h are off by h^2 / 6 times the third
     # derivative and by the loss's own error over h

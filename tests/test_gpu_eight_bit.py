@@ -132,7 +132,7 @@ def test_quantize_extreme_values(block, dtype):
 @pytest.mark.parametrize("dtype", TYPES)
 def test_quantize_strided_and_unaligned_rows(block, dtype):
     big = _x(150, 700, dtype, 4)
-    for x in (big[3:140, 5:400], big[:, 8:520], big[::2, 1:2], big[7:8, 3:300]):
+    for x in (big[3:140, 5:400], big[:, 8:520], big[::2, 1:2], big[7:8, 3:300], big[:, 571:], big[1:, 442:699]):
         _check_quantized(tsl.tsenor_quantize(x, block), x, block)
 
 
@@ -202,6 +202,10 @@ def _check_product(out, want, size, k):
 
 SIZES = [(1, 1, 1), (1, 128, 128), (3, 5, 7), (64, 64, 512), (128, 128, 129), (130, 260, 520), (1, 1000, 640), (17, 96, 33),
          (257, 300, 1111), (700, 1100, 900), (512, 768, 1024), (31, 4100, 2050), (300, 64, 4000), (1, 300, 20000)]
+
+
+# more tiles than SMs, so that a block walks several; more blocks of 128 than a ring holds
+SIZES += [(64, 25000, 300), (2600, 3100, 520), (100, 200, 30000), (1000, 4100, 2000)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
