@@ -126,7 +126,8 @@ tsenor_status tsenor_objective(const void* W, tsenor_dtype dtype, int64_t rows, 
  * Synchronises `stream`, then returns in *count_out the number of blocks that
  * failed on this device (non-finite input, or a rounding step that found no
  * move) since the previous call, and of rows that failed in the distillation
- * calls, and resets the counter.  Returns TSENOR_OK
+ * calls, and resets the counter.  (A kernel of the products or of the
+ * distillation whose bounded wait ran out counts too; its results are not valid.)  Returns TSENOR_OK
  * when that number is 0 and TSENOR_ERR_DEVICE when it is not (the count is
  * written in both cases); TSENOR_ERR_ARG for a null count_out, TSENOR_ERR_CUDA
  * when the copy or the synchronisation fails.
@@ -378,7 +379,7 @@ tsenor_status tsenor_matmul(tsenor_form form, const uint8_t* a, int64_t lda, con
  * grad has the type of the logits, ldg elements from row to row; it may be
  * the logits' own memory (same pointer, ldg == ld).  The sums are fp32 in a
  * fixed order: the same call gives the same bits.  TSENOR_ERR_SHAPE for top,
- * vocab or rows (2^24) above the limits.
+ * vocab or rows (2^24) above the limits; 1e-6 <= temperature <= 3e38.
  */
 #define TSENOR_DISTILL_MAX_TOP 1024
 #define TSENOR_DISTILL_MAX_VOCAB 262144
