@@ -146,19 +146,25 @@ struct Plus {
     __device__ double operator()(double a, double b) const { return a + b; }
 };
 
+// log of a sum of 1 or more in fp64: the exponent apart, so that logf sees [1, 2).
+__device__ __forceinline__ double log_sum(float s) {
+    const int e = int(__float_as_uint(s) >> 23) - 127;
+    return double(e) * 0.6931471805599453 + double(logf(__uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u)));
+}
+
 // The teacher's entries of a row in shared memory, their number rounded up to 4.
 template <typename TEAM, int N>
 struct Teacher {
     int top, top4, slots;
-    float* logp;                                 // t_j / T until weights() has run
+    float* t;                                    // the teacher's logits; -inf: no entry
     float* p;
     int* index;                                  // 16-byte aligned; -1: no entry
     int* table;                                  // of the indices seen, open addressing; `slots` a power of two
     float* logit;                                // the student's logits of the entries' columns
 
     __device__ Teacher(void* at, int top_, int slots_) : top(top_), top4((top_ + 3) / 4 * 4), slots(slots_) {
-        logp = static_cast<float*>(at);
-        p = logp + top4;
+        t = static_cast<float*>(at);
+        p = t + top4;
         index = reinterpret_cast<int*>(p + top4);
         table = index + top4;
         logit = reinterpret_cast<float*>(table + slots);
@@ -170,12 +176,12 @@ struct Teacher {
         bool wrong = a.teacher_lse && !(fabsf(a.teacher_lse[row]) < INFINITY), any = false;
         for (int j = TEAM::id(); j < top4; j += N) {
             const int i = j < top ? a.index[row * top + j] : -1;
-            const float v = j < top ? a.top_logits[row * top + j] / a.temperature : 0.f;
+            const float v = j < top ? a.top_logits[row * top + j] : 0.f;
             const bool in = i >= 0 && i < a.vocab;
             wrong = wrong || (i >= 0 && !(in && v < INFINITY));
             any = any || (in && v > -INFINITY) || i >= a.vocab || (i >= 0 && v != v);
             index[j] = in ? i : -1;
-            logp[j] = in ? v : -INFINITY;
+            t[j] = in ? v : -INFINITY;
         }
         *empty = !TEAM::any(any);
         *bad = TEAM::any(wrong) && !*empty;
@@ -205,22 +211,20 @@ struct Teacher {
     }
     static constexpr int kTwin = 1 << 30;        // above every column
     __device__ static unsigned first_slot(int v) { return (unsigned(v) * 2654435761u) >> 7; }
-    // After read_entries: log p and p of this thread's entries; P = sum p.  `red`: 3 N / 32 values.
-    __device__ float weights(const DistillArgs& a, int64_t row, float* red) const {
-        float c;
+    // After read_entries: p of this thread's entries; P = sum p, and c of log p_j = t_j / T - c.  `red`: 3 N / 32 values.
+    __device__ float weights(const DistillArgs& a, int64_t row, float* red, double* c) const {
         if (a.teacher_lse) {
-            c = a.teacher_lse[row];
+            *c = double(a.teacher_lse[row]);
         } else {
             float high = -INFINITY, sum = 0.f;
-            for (int j = TEAM::id(); j < top; j += N) high = fmaxf(high, logp[j]);
+            for (int j = TEAM::id(); j < top; j += N) high = fmaxf(high, t[j]);
             high = TEAM::reduce(high, red, Larger());
-            for (int j = TEAM::id(); j < top; j += N) sum += expf(logp[j] - high);
-            c = high + logf(TEAM::reduce(sum, red + N / 32, Plus()));
+            for (int j = TEAM::id(); j < top; j += N) sum += expf(float(double(t[j] - high) * a.inv_t));
+            *c = double(high) * a.inv_t + log_sum(TEAM::reduce(sum, red + N / 32, Plus()));
         }
         float total = 0.f;
         for (int j = TEAM::id(); j < top4; j += N) {
-            const float l = logp[j] - c, w = expf(l);
-            logp[j] = l;
+            const float w = t[j] == -INFINITY ? 0.f : expf(float(double(t[j]) * a.inv_t - *c));
             p[j] = w;
             total += w;
         }
@@ -303,12 +307,6 @@ __device__ __forceinline__ Norm join(int n, float scale2, F get) {
     }
     return all;
 }
-// log of a sum of 1 or more in fp64: the exponent apart, so that logf sees [1, 2).
-__device__ __forceinline__ double log_sum(float s) {
-    const int e = int(__float_as_uint(s) >> 23) - 127;
-    return double(e) * 0.6931471805599453 + double(logf(__uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u)));
-}
-
 // Adds n chunks to a normaliser: their maximum first, so that one step of the running maximum serves them all.
 template <typename T, int n>
 __device__ __forceinline__ void take(Norm& norm, const uint4* v, float scale2) {
@@ -362,35 +360,45 @@ __device__ __forceinline__ Norm warp_join(Norm norm, float scale2) {
     return Norm{high, norm.sum};
 }
 
-// This slice's part of sum_j p_j (log p_j - z_j / T), and the entries' logits, by the threads of a team.
+// A row's loss is T^2 (sum_j p_j (log p_j - z_j / T) + lse sum_j p_j): both sums, over a slice's entries, in fp64, since they
+// all but cancel where the student is near its teacher.
+struct Terms {
+    double gap, mass;
+};
+// By the threads of a team, which also keep the entries' logits.  `red`: 2 N / 32 values.
 template <typename T, typename TEAM, int N>
-__device__ double team_term(const DistillArgs& a, const typename T::storage* z, const Slice<T>& slice,
-                            const Teacher<TEAM, N>& teacher, double* red) {
-    double term = 0.0;
+__device__ Terms team_terms(const DistillArgs& a, const typename T::storage* z, const Slice<T>& slice,
+                            const Teacher<TEAM, N>& teacher, double c, double* red) {
+    Terms s{0.0, 0.0};
     for (int j = TEAM::id(); j < a.top; j += N) {
         const int v = teacher.index[j];
         const float w = teacher.p[j];
         if (v < 0 || !slice.has(v)) continue;
         const float x = read<T>(z + v);
         teacher.logit[j] = x;
-        if (w > 0.f) term += double(w) * (double(teacher.logp[j]) - double(x) * a.inv_t);
+        if (w > 0.f) {
+            s.gap += double(w) * ((double(teacher.t[j]) - double(x)) * a.inv_t - c);
+            s.mass += double(w);
+        }
     }
-    return TEAM::reduce(term, red, Plus());
+    s.gap = TEAM::reduce(s.gap, red, Plus());
+    s.mass = TEAM::reduce(s.mass, red + N / 32, Plus());
+    return s;
 }
 
 // What a slice tells the others of its row.
-struct Share {
+struct alignas(16) Share {
+    Terms terms;
     Norm norm;
-    double term;
 };
 
 // One thread: the row's loss (and lse), its failure.
 template <bool STEP>
-__device__ void write_loss(const DistillArgs& a, int64_t row, Norm norm, double term, float total, bool empty, bool failed) {
+__device__ void write_loss(const DistillArgs& a, int64_t row, Norm norm, Terms s, bool empty, bool failed) {
     const double lse = norm.high == -INFINITY ? double(norm.high + norm.sum)      // no finite logit: -inf, or NaN
                                               : double(norm.high) * a.inv_t + log_sum(norm.sum);
     a.loss[row] = failed ? NAN : empty ? 0.f
-                  : float(double(a.temperature) * double(a.temperature) * (term + double(total) * lse));
+                  : float(double(a.temperature) * double(a.temperature) * (s.gap + s.mass * lse));
     if (!STEP) a.lse[row] = failed ? NAN : float(lse);
     if (failed) atomicAdd(&g_row_failures, 1ull);
 }
@@ -410,7 +418,8 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
     constexpr int kPer = Slice<T>::kPer;
     __shared__ Share share[2][kMaxSlices];
     __shared__ Norm part[2][kWarps];
-    __shared__ double red64[kTeachers / 32], term_of_slice[2];
+    __shared__ double red64[2 * kTeachers / 32];
+    __shared__ Terms terms_of_slice[2];
     __shared__ float red[3 * kTeachers / 32], total_of_p[2], extra[2][2 * kPer];
     __shared__ int flags[2];                     // 1: no entry, 2: the row fails
     __shared__ float row_high[2], row_scale[2], row_by[2];                    // of a row's gradient; by 0: it is 0
@@ -482,11 +491,12 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
             if (e < slice.extras()) extra[b][e] = read<T>(z + slice.extra(e));
             if (!empty && !(STEP && bad)) {
                 if (STEP) teacher.mark_twins();
-                const float total = teacher.weights(a, row, red);
-                const double term = team_term<T, Extra, kTeachers>(a, z, slice, teacher, red64);
+                double c;
+                const float total = teacher.weights(a, row, red, &c);
+                const Terms terms = team_terms<T>(a, z, slice, teacher, c, red64);
                 if (t == kThreads) {
                     total_of_p[b] = total;
-                    term_of_slice[b] = term;
+                    terms_of_slice[b] = terms;
                 }
             }
             __syncwarp();
@@ -559,26 +569,29 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
             if (lane == 0) part[b][warp] = norm;
             Workers::sync();
             norm = join(kWarps, scale2, [&](int k) { return part[b][k]; });
-            double term = empty ? 0.0 : term_of_slice[b];
+            Terms terms = empty ? Terms{0.0, 0.0} : terms_of_slice[b];
             const float total = empty ? 0.f : total_of_p[b];
             if (slices > 1) {
                 const int j = joins & 1;
                 if (t < slices) {
                     const uint32_t to = cluster_addr(smem_u32(&share[j][rank]), t);
-                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(norm.high), "f"(norm.sum) : "memory");
-                    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to + 8), "d"(term) : "memory");
+                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to + 16), "f"(norm.high), "f"(norm.sum) : "memory");
+                    asm volatile("st.shared::cluster.v2.f64 [%0], {%1, %2};" ::"r"(to), "d"(terms.gap), "d"(terms.mass) : "memory");
                     cluster_arrive(cluster_addr(smem_u32(joined + j), t));
                 }
                 if (!mbar_cluster_sleep_bounded(joined + j, (joins >> 1) & 1)) stalled = true;
                 if (Workers::any(stalled)) { stalled = true; break; }
                 ++joins;
                 norm = join(slices, scale2, [&](int k) { return share[j][k].norm; });
-                term = 0.0;
-                for (int k = 0; k < slices; ++k) term += share[j][k].term;
+                terms = Terms{0.0, 0.0};
+                for (int k = 0; k < slices; ++k) {
+                    terms.gap += share[j][k].terms.gap;
+                    terms.mass += share[j][k].terms.mass;
+                }
             }
             const float m = norm.high;
             failed = failed || (!empty && !(fabsf(m) < INFINITY && norm.sum < INFINITY));
-            if (t == 0 && rank == 0) write_loss<STEP>(a, row, norm, term, total, empty, failed);
+            if (t == 0 && rank == 0) write_loss<STEP>(a, row, norm, terms, empty, failed);
             if constexpr (STEP) {
                 const float by = a.temperature * (a.weight ? a.weight[row] : 1.f);
                 if (failed || by == 0.f) {
@@ -627,11 +640,12 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
 // (the second time from L2, last chunks first).  Nothing of a row waits for another SM, and a row's fixed costs
 // are paid once.
 template <typename T, bool STEP>
-__global__ void __launch_bounds__(kThreads + kTeachers, 5)
+__global__ void __launch_bounds__(kThreads + kTeachers, STEP ? 5 : 4)
 stream_kernel(const DistillArgs a, const int slots) {
     extern __shared__ __align__(128) uint4 room[];
     __shared__ Norm part[kWarps];
-    __shared__ double term_of_row, red64[kTeachers / 32];
+    __shared__ double red64[2 * kTeachers / 32];
+    __shared__ Terms terms_of_row;
     __shared__ float total_of_p, red[3 * kTeachers / 32];
     __shared__ int flags;                        // 1: no entry, 2: the row fails
     constexpr int kPer = Slice<T>::kPer;
@@ -654,11 +668,12 @@ stream_kernel(const DistillArgs a, const int slots) {
         if (STEP) __syncthreads();
         if (!empty && !(STEP && bad)) {
             if (STEP) teacher.mark_twins();
-            const float total = teacher.weights(a, row, red);
-            const double term = team_term<T, Extra, kTeachers>(a, z, slice, teacher, red64);
+            double c;
+            const float total = teacher.weights(a, row, red, &c);
+            const Terms terms = team_terms<T>(a, z, slice, teacher, c, red64);
             if (t == kThreads) {
                 total_of_p = total;
-                term_of_row = term;
+                terms_of_row = terms;
             }
         }
     } else {
@@ -696,7 +711,7 @@ stream_kernel(const DistillArgs a, const int slots) {
     const Norm norm = join(kWarps, scale2, [&](int k) { return part[k]; });
     const float m = norm.high;
     failed = failed || (!empty && !(fabsf(m) < INFINITY && norm.sum < INFINITY));
-    if (t == kThreads) write_loss<STEP>(a, row, norm, term_of_row, total_of_p, empty, failed);
+    if (t == kThreads) write_loss<STEP>(a, row, norm, empty ? Terms{0.0, 0.0} : terms_of_row, empty, failed);
     if constexpr (STEP) {
         const float by = a.temperature * (a.weight ? a.weight[row] : 1.f);
         if (failed || by == 0.f) {
@@ -743,7 +758,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
     const Slice<T> slice(z, int(a.vocab), rank, slices);
     Teacher<Team<0, kThreads, 1>, kThreads> teacher(room, a.top, slots);
-    float* target = teacher.logp;                // log p is not needed here
+    float* target = teacher.logit;               // the gradients of the entries' columns
     const bool vec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     let_next_start();
     prior_done();
@@ -766,7 +781,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     };
     load(t);                                     // on their way while the weights are made
     teacher.mark_twins();
-    const float total = teacher.weights(a, row, red);
+    double c;
+    const float total = teacher.weights(a, row, red, &c);
     __syncthreads();
     const float inv_t = 1.f / a.temperature, scale = by * total;
     auto at = [&](float x) { return scale * ex2(fmaf(x, inv_t, -lse) * kLog2E); };
@@ -799,7 +815,7 @@ int slices_of(int64_t rows, int64_t row_bytes) {
 }
 
 // Streaming pays where a row's fixed costs weigh more than a second read: for the loss
-// (which has none) wherever the rows fill the device, 95 us against 139 for 2048 x 131072 bf16; for the step with
+// (which has none) wherever the rows fill the device, 93 us against 139 for 2048 x 131072 bf16; for the step with
 // short rows, 36 us against 57 for 4096 x 1000 and 13 against 18 for 512 x 10000, but 65 against 58 for
 // 2048 x 32000.
 bool streams(bool step, int64_t rows, int64_t row_bytes) { return rows >= 148 && (!step || row_bytes <= 32 * 1024); }
