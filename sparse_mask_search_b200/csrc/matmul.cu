@@ -1,6 +1,13 @@
 // Product of two e4m3 matrices with a power-of-two scale per block of 128 along
 // the contracted axis:
 //   nt  out[m,n] = sum_k A[m,k] B[n,k]     nn  A[m,k] B[k,n]     tn  A[k,m] B[k,n]
+//
+// The scales are exponents, so the tensor cores apply them (kind::mxf8f6f4, one byte per row and 32 of the
+// contracted axis; the same byte for four such steps): sums stay in tensor memory in fp32 from the first block to
+// the last and are rounded once.  Codes stored along either axis are read as they are, K-major or MN-major.
+// Bound by the tensor cores (and, on random data, by the card's power limit) for many rows, by the bytes
+// of B for few.  Measured, with the host's share: 4096 x 28672 x 8192 nt 764 us (2.52 PFLOP/s; 486 us on zeros, where
+// the clock stays at 1965 MHz), 2048 x 11008 x 4096 84 us, 1 x 11008 x 4096 12.3 us (3.7 TB/s).
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -36,7 +43,7 @@ constexpr int kScaleBytes = 512;
 constexpr int kSms = 148;
 constexpr int kPad = 132;                        // floats to a staged row: 16-byte stores without bank conflicts
 
-// The products issue and load loops may wait for as long as a tile's sums take.
+// An epilogue waits for as long as a tile's sums take: the bound grows with their number.
 __device__ __forceinline__ bool wait_long(uint64_t* bar, unsigned parity, int64_t blocks) {
     for (int64_t i = 0; i <= blocks / 64; ++i)
         if (mbar_sleep_bounded(bar, parity)) return true;
@@ -363,7 +370,9 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 // persistent.  Two accumulators of 256 columns and the scales do not fit into
 // 512 columns of tensor memory, so the second one starts at column 240: its
 // product may start once the 32 columns that hold the overlap have been read, which
-// the epilogue does first.
+// the epilogue does first.  A 256 x 256 tile, because each byte that an SM takes in is used by one product only:
+// at 128 x 128 the loads alone (64 bytes a cycle and SM) took twice the products' time, here they take as long.
+// Between the two kernels the fitted costs at `launch` decide.  Five stages or four or six make no difference.
 constexpr int kPairThreads = 384;                // warps: 0 loads, 1 products, 2 tensor memory, 4 to 11 epilogue
 constexpr int kPairTile = 256;
 constexpr int kPairStages = 5;
