@@ -153,28 +153,30 @@ __device__ __forceinline__ double log_sum(float s) {
     return double(e) * 0.6931471805599453 + double(logf(__uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u)));
 }
 
-// The teacher's entries of a row in shared memory, their number rounded up to 4.
+// The teacher's entries of a row in shared memory, their number rounded up to 4, and a table to find equal indices,
+// which is free again once mark_twins(slice) has run.
 template <typename TEAM, int N>
 struct Teacher {
     int top, top4, slots;
-    float* t;                                    // the teacher's logits; -inf: no entry
+    float* t;                                    // the teacher's logits (-inf: no entry)
+    float* logit;                                // in the same place: the student's logits of the entries' columns
     float* p;
-    int* index;                                  // 16-byte aligned; -1: no entry
-    int* table;                                  // of the indices seen, open addressing; `slots` a power of two
-    float* logit;                                // the student's logits of the entries' columns
+    int* index;                                  // 16-byte aligned; -1: no entry; kTwin set: another entry has it too
+    int* table;                                  // of the indices in the slice, open addressing; `slots` a power of two
+    static constexpr int kTwin = 1 << 30;        // above every column
 
-    __device__ Teacher(void* at, int top_, int slots_) : top(top_), top4((top_ + 3) / 4 * 4), slots(slots_) {
-        t = static_cast<float*>(at);
+    __device__ Teacher(void* at, int* table_, int top_, int slots_)
+        : top(top_), top4((top_ + 3) / 4 * 4), slots(slots_), table(table_) {
+        t = logit = static_cast<float*>(at);
         p = t + top4;
         index = reinterpret_cast<int*>(p + top4);
-        table = index + top4;
-        logit = reinterpret_cast<float*>(table + slots);
     }
 
     // Reads the entries; empty: none has weight, bad: the row fails.
     __device__ void read_entries(const DistillArgs& a, int64_t row, bool* empty, bool* bad) {
         for (int i = TEAM::id(); i < slots; i += N) table[i] = -1;
         bool wrong = a.teacher_lse && !(fabsf(a.teacher_lse[row]) < INFINITY), any = false;
+#pragma unroll 4
         for (int j = TEAM::id(); j < top4; j += N) {
             const int i = j < top ? a.index[row * top + j] : -1;
             const float v = j < top ? a.top_logits[row * top + j] : 0.f;
@@ -187,31 +189,36 @@ struct Teacher {
         *empty = !TEAM::any(any);
         *bad = TEAM::any(wrong) && !*empty;
     }
-    // After read_entries: marks the indices that more than one entry has.
-    __device__ void mark_twins() const {
+    // After read_entries: marks the entries in the slice whose index another entry has too.
+    template <typename S>
+    __device__ void mark_twins(const S& slice) const {
+        auto slot = [&](int v, int k) { return table + ((((unsigned(v) * 2654435761u) >> 7) + k) & (slots - 1)); };
+        bool met = false;
         for (int j = TEAM::id(); j < top; j += N) {
             const int v = index[j];
-            if (v < 0) continue;
+            if (v < 0 || !slice.has(v)) continue;
             for (int k = 0; k < slots; ++k) {                                // half of the slots stay free
-                int* slot = table + ((first_slot(v) + k) & (slots - 1));
-                const int was = atomicCAS(slot, -1, v);
+                const int was = atomicCAS(slot(v, k), -1, v);
                 if (was == -1) break;
                 if ((was & ~kTwin) == v) {
-                    atomicOr(slot, kTwin);
+                    atomicOr(slot(v, k), kTwin);
+                    met = true;
                     break;
                 }
             }
         }
-    }
-    __device__ bool has_twin(int v) const {
-        for (int k = 0; k < slots; ++k) {
-            const int was = table[(first_slot(v) + k) & (slots - 1)];
-            if ((was & ~kTwin) == v) return was & kTwin;
+        if (!TEAM::any(met)) return;             // as a rule
+        for (int j = TEAM::id(); j < top; j += N) {
+            const int v = index[j];
+            if (v < 0 || !slice.has(v)) continue;
+            for (int k = 0; k < slots; ++k) {
+                const int was = *slot(v, k);
+                if ((was & ~kTwin) != v) continue;
+                index[j] = was;
+                break;
+            }
         }
-        return false;
     }
-    static constexpr int kTwin = 1 << 30;        // above every column
-    __device__ static unsigned first_slot(int v) { return (unsigned(v) * 2654435761u) >> 7; }
     // After read_entries: p of this thread's entries; P = sum p, and c of log p_j = t_j / T - c.  `red`: 3 N / 32 values.
     __device__ float weights(const DistillArgs& a, int64_t row, float* red, double* c) const {
         if (a.teacher_lse) {
@@ -220,10 +227,12 @@ struct Teacher {
             float high = -INFINITY, sum = 0.f;
             for (int j = TEAM::id(); j < top; j += N) high = fmaxf(high, t[j]);
             high = TEAM::reduce(high, red, Larger());
+#pragma unroll 4
             for (int j = TEAM::id(); j < top; j += N) sum += expf(float(double(t[j] - high) * a.inv_t));
             *c = double(high) * a.inv_t + log_sum(TEAM::reduce(sum, red + N / 32, Plus()));
         }
         float total = 0.f;
+#pragma unroll 4
         for (int j = TEAM::id(); j < top4; j += N) {
             const float w = t[j] == -INFINITY ? 0.f : expf(float(double(t[j]) * a.inv_t - *c));
             p[j] = w;
@@ -235,18 +244,18 @@ struct Teacher {
     template <int M, typename S, typename F>
     __device__ __forceinline__ void each(int me, const S& slice, F f) const {
         for (int j = me; j < top; j += M) {
-            const int v = index[j];
-            if (v < 0 || !slice.has(v)) continue;
+            const int i = index[j], v = i & ~kTwin;
+            if (i < 0 || !slice.has(v)) continue;
             bool first = true;
             float w = p[j];
-            if (has_twin(v)) {                   // in the order of the entries
+            if (i & kTwin) {                     // in the order of the entries
                 w = 0.f;
                 for (int k = 0; k < top4; k += 4) {
                     const int4 o = *reinterpret_cast<const int4*>(index + k);
-                    if (o.x == v) { first = first && k >= j; w += p[k]; }
-                    if (o.y == v) { first = first && k + 1 >= j; w += p[k + 1]; }
-                    if (o.z == v) { first = first && k + 2 >= j; w += p[k + 2]; }
-                    if (o.w == v) { first = first && k + 3 >= j; w += p[k + 3]; }
+                    if (o.x == i) { first = first && k >= j; w += p[k]; }
+                    if (o.y == i) { first = first && k + 1 >= j; w += p[k + 1]; }
+                    if (o.z == i) { first = first && k + 2 >= j; w += p[k + 2]; }
+                    if (o.w == i) { first = first && k + 3 >= j; w += p[k + 3]; }
                 }
             }
             if (first) f(j, v, w);
@@ -259,7 +268,8 @@ int slots_of(int top) {
     while (n < 2 * top) n *= 2;
     return n;
 }
-unsigned teacher_bytes(int top) { return unsigned((top + 3) / 4 * 4 * 16 + slots_of(top) * 4); }
+// Shared memory of `rows` rows' entries and a table.
+unsigned teacher_bytes(int top, int rows) { return unsigned(rows * ((top + 3) / 4 * 4) * 12 + slots_of(top) * 4); }
 
 // Gradient 0 for the columns of a slice.
 template <typename T, int M>
@@ -371,16 +381,17 @@ template <typename T, typename TEAM, int N>
 __device__ Terms team_terms(const DistillArgs& a, const typename T::storage* z, const Slice<T>& slice,
                             const Teacher<TEAM, N>& teacher, double c, double* red) {
     Terms s{0.0, 0.0};
+#pragma unroll 4
     for (int j = TEAM::id(); j < a.top; j += N) {
-        const int v = teacher.index[j];
+        const int i = teacher.index[j], v = i & ~Teacher<TEAM, N>::kTwin;
         const float w = teacher.p[j];
-        if (v < 0 || !slice.has(v)) continue;
+        if (i < 0 || !slice.has(v)) continue;
         const float x = read<T>(z + v);
-        teacher.logit[j] = x;
         if (w > 0.f) {
             s.gap += double(w) * ((double(teacher.t[j]) - double(x)) * a.inv_t - c);
             s.mass += double(w);
         }
+        teacher.logit[j] = x;
     }
     s.gap = TEAM::reduce(s.gap, red, Plus());
     s.mass = TEAM::reduce(s.mass, red + N / 32, Plus());
@@ -414,7 +425,7 @@ __device__ void write_loss(const DistillArgs& a, int64_t row, Norm norm, Terms s
 // 2048 x 131072 bf16 227 us (4.7 TB/s), 1024 x 131072 fp32 205 us (5.2 TB/s; 227 with a CTA for each slice of each row).
 template <typename T, bool STEP>
 __global__ void __launch_bounds__(kThreads + kTeachers, 3)
-loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const int slots, const int teacher_room) {
+loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const int slots) {
     extern __shared__ __align__(128) uint4 chunk[];
     constexpr int kPer = Slice<T>::kPer;
     __shared__ Share share[2][kMaxSlices];
@@ -450,7 +461,9 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
     prior_done();
     auto row_of = [&](int64_t row) { return static_cast<const typename T::storage*>(a.logits) + row * a.ld; };
     auto teacher_of = [&](int b) {
-        return Teacher<Extra, kTeachers>(reinterpret_cast<uint8_t*>(chunk + chunk_room) + b * teacher_room, a.top, slots);
+        float* at = reinterpret_cast<float*>(chunk + chunk_room);
+        const int words = (a.top + 3) / 4 * 4 * 3;
+        return Teacher<Extra, kTeachers>(at + b * words, reinterpret_cast<int*>(at + 2 * words), a.top, slots);
     };
     bool stalled = false;
 
@@ -491,7 +504,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
             const int e = t - kThreads;
             if (e < slice.extras()) extra[b][e] = read<T>(z + slice.extra(e));
             if (!empty && !(STEP && bad)) {
-                if (STEP) teacher.mark_twins();
+                if (STEP) teacher.mark_twins(slice);
                 double c;
                 const float total = teacher.weights(a, row, red, &c);
                 const Terms terms = team_terms<T>(a, z, slice, teacher, c, red64);
@@ -656,7 +669,7 @@ stream_kernel(const DistillArgs a, const int slots) {
     auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
     const Slice<T> slice(z, int(a.vocab), 0, 1);
     using Extra = Team<kThreads, kTeachers, 1>;
-    Teacher<Extra, kTeachers> teacher(room, a.top, slots);
+    Teacher<Extra, kTeachers> teacher(room, reinterpret_cast<int*>(room) + (a.top + 3) / 4 * 4 * 3, a.top, slots);
     const bool vec = STEP && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     const float inv_t = 1.f / a.temperature, scale2 = inv_t * kLog2E;
     const uint4* in = reinterpret_cast<const uint4*>(z + slice.first);
@@ -668,7 +681,7 @@ stream_kernel(const DistillArgs a, const int slots) {
         if (t == kThreads) flags = (empty ? 1 : 0) | (bad ? 2 : 0);
         if (STEP) __syncthreads();
         if (!empty && !(STEP && bad)) {
-            if (STEP) teacher.mark_twins();
+            if (STEP) teacher.mark_twins(slice);
             double c;
             const float total = teacher.weights(a, row, red, &c);
             const Terms terms = team_terms<T>(a, z, slice, teacher, c, red64);
@@ -758,7 +771,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     const auto* z = static_cast<const typename T::storage*>(a.logits) + row * a.ld;
     auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
     const Slice<T> slice(z, int(a.vocab), rank, slices);
-    Teacher<Team<0, kThreads, 1>, kThreads> teacher(room, a.top, slots);
+    Teacher<Team<0, kThreads, 1>, kThreads> teacher(room, reinterpret_cast<int*>(room) + (a.top + 3) / 4 * 4 * 3, a.top, slots);
     float* target = teacher.logit;               // the gradients of the entries' columns
     const bool vec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     let_next_start();
@@ -781,7 +794,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
             if (c + i * kThreads < slice.chunks) v[i] = in[c + i * kThreads];
     };
     load(t);                                     // on their way while the weights are made
-    teacher.mark_twins();
+    teacher.mark_twins(slice);
     double c;
     const float total = teacher.weights(a, row, red, &c);
     __syncthreads();
@@ -825,12 +838,12 @@ template <typename T, bool STEP>
 cudaError_t launch_loss(const DistillArgs& a, cudaStream_t st) {
     const int64_t row_bytes = a.vocab * int64_t(sizeof(typename T::storage));
     if (streams(STEP, a.rows, row_bytes)) {
-        return launch_early(stream_kernel<T, STEP>, a.rows, kThreads + kTeachers, teacher_bytes(a.top), 1, st, a,
+        return launch_early(stream_kernel<T, STEP>, a.rows, kThreads + kTeachers, teacher_bytes(a.top, 1), 1, st, a,
                             slots_of(a.top));
     }
     const int slices = slices_of(a.rows, row_bytes);
     const int chunk_room = int((row_bytes / 16 + slices - 1) / slices);
-    const unsigned teacher_room = (teacher_bytes(a.top) + 15) / 16 * 16, bytes = unsigned(chunk_room * 16) + 2 * teacher_room;
+    const unsigned bytes = unsigned(chunk_room * 16) + teacher_bytes(a.top, 2);
     cudaError_t e = cudaFuncSetAttribute(loss_kernel<T, STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
     // No more clusters than run at once, or the last ones would start when the others are through.
@@ -842,7 +855,7 @@ cudaError_t launch_loss(const DistillArgs& a, cudaStream_t st) {
         if (fit > 0 && clusters > fit) clusters = fit;
     }
     return launch_early(loss_kernel<T, STEP>, clusters * slices, kThreads + kTeachers, bytes, slices, st, a, slices, chunk_room,
-                        slots_of(a.top), int(teacher_room));
+                        slots_of(a.top));
 }
 
 template <typename T>
@@ -851,7 +864,7 @@ cudaError_t launch_grad(const DistillArgs& a, cudaStream_t st) {
     const int64_t row_bytes = a.vocab * int64_t(sizeof(typename T::storage));
     const int slices = a.rows >= 296 ? int((row_bytes + kSliceBytes - 1) / kSliceBytes)
                                      : int((row_bytes + kSliceBytes / 8 - 1) / (kSliceBytes / 8));
-    return launch_early(grad_kernel<T>, a.rows * slices, kThreads, teacher_bytes(a.top), 1, st, a, slices, slots_of(a.top));
+    return launch_early(grad_kernel<T>, a.rows * slices, kThreads, teacher_bytes(a.top, 1), 1, st, a, slices, slots_of(a.top));
 }
 
 tsenor_status finish(cudaError_t e, const char* what) { return e == cudaSuccess ? TSENOR_OK : cuda_fail(e, what); }
