@@ -115,6 +115,8 @@ struct Slice {
     }
 };
 
+__device__ __forceinline__ float shuffle_xor(float v, int lane) { return __shfl_xor_sync(kFullMask, v, lane); }
+
 // N threads of a block, from thread FIRST on, that meet at the block's barrier ID.
 template <int FIRST, int N, int ID>
 struct Team {
@@ -130,7 +132,7 @@ struct Team {
     template <typename X, typename F>
     __device__ static X reduce(X v, X* red, F f) {
 #pragma unroll
-        for (int s = 16; s >= 1; s >>= 1) v = f(v, __shfl_xor_sync(kFullMask, v, s));
+        for (int s = 16; s >= 1; s >>= 1) v = f(v, shuffle_xor(v, s));
         if ((threadIdx.x & 31) == 0) red[id() / 32] = v;
         sync();
         v = red[0];
@@ -143,8 +145,8 @@ struct Larger {
     __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
 struct Plus {
-    __device__ float operator()(float a, float b) const { return a + b; }
-    __device__ double operator()(double a, double b) const { return a + b; }
+    template <typename X>
+    __device__ X operator()(X a, X b) const { return a + b; }
 };
 
 // log of a sum of 1 or more in fp64: the exponent apart, so that logf sees [1, 2).
@@ -219,26 +221,27 @@ struct Teacher {
             }
         }
     }
-    // After read_entries: p of this thread's entries; P = sum p, and c of log p_j = t_j / T - c.  `red`: 3 N / 32 values.
+    // After read_entries: p of this thread's entries; P = sum p, and c of log p_j = t_j / T - c.  `red`: 2 N / 32 values.
     __device__ float weights(const DistillArgs& a, int64_t row, float* red, double* c) const {
+        float total = 1.f;                       // of a softmax over the entries
         if (a.teacher_lse) {
             *c = double(a.teacher_lse[row]);
         } else {
+            const float inv_t = 1.f / a.temperature;
             float high = -INFINITY, sum = 0.f;
             for (int j = TEAM::id(); j < top; j += N) high = fmaxf(high, t[j]);
             high = TEAM::reduce(high, red, Larger());
-#pragma unroll 4
-            for (int j = TEAM::id(); j < top; j += N) sum += expf(float(double(t[j] - high) * a.inv_t));
+            for (int j = TEAM::id(); j < top; j += N) sum += expf((t[j] - high) * inv_t);
             *c = double(high) * a.inv_t + log_sum(TEAM::reduce(sum, red + N / 32, Plus()));
         }
-        float total = 0.f;
-#pragma unroll 4
+        float part = 0.f;
         for (int j = TEAM::id(); j < top4; j += N) {
             const float w = t[j] == -INFINITY ? 0.f : expf(float(double(t[j]) * a.inv_t - *c));
             p[j] = w;
-            total += w;
+            part += w;
         }
-        return TEAM::reduce(total, red + 2 * (N / 32), Plus());
+        if (a.teacher_lse) total = TEAM::reduce(part, red, Plus());
+        return total;
     }
     // Thread `me` of M: f(j, v, sum of the weights of index v) for the entries in a slice, each index once.
     template <int M, typename S, typename F>
@@ -375,11 +378,15 @@ __device__ __forceinline__ Norm warp_join(Norm norm, float scale2) {
 // all but cancel where the student is near its teacher.
 struct Terms {
     double gap, mass;
+    __device__ Terms operator+(Terms o) const { return Terms{gap + o.gap, mass + o.mass}; }
 };
-// By the threads of a team, which also keep the entries' logits.  `red`: 2 N / 32 values.
+__device__ __forceinline__ Terms shuffle_xor(Terms s, int lane) {
+    return Terms{__shfl_xor_sync(kFullMask, s.gap, lane), __shfl_xor_sync(kFullMask, s.mass, lane)};
+}
+// By the threads of a team, which also keep the entries' logits.  `red`: N / 32 values.
 template <typename T, typename TEAM, int N>
 __device__ Terms team_terms(const DistillArgs& a, const typename T::storage* z, const Slice<T>& slice,
-                            const Teacher<TEAM, N>& teacher, double c, double* red) {
+                            const Teacher<TEAM, N>& teacher, double c, Terms* red) {
     Terms s{0.0, 0.0};
 #pragma unroll 4
     for (int j = TEAM::id(); j < a.top; j += N) {
@@ -393,9 +400,7 @@ __device__ Terms team_terms(const DistillArgs& a, const typename T::storage* z, 
         }
         teacher.logit[j] = x;
     }
-    s.gap = TEAM::reduce(s.gap, red, Plus());
-    s.mass = TEAM::reduce(s.mass, red + N / 32, Plus());
-    return s;
+    return TEAM::reduce(s, red, Plus());
 }
 
 // What a slice tells the others of its row.
@@ -430,9 +435,8 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
     constexpr int kPer = Slice<T>::kPer;
     __shared__ Share share[2][kMaxSlices];
     __shared__ Norm part[2][kWarps];
-    __shared__ double red64[2 * kTeachers / 32];
-    __shared__ Terms terms_of_slice[2];
-    __shared__ float red[3 * kTeachers / 32], total_of_p[2], extra[2][2 * kPer];
+    __shared__ Terms red64[kTeachers / 32], terms_of_slice[2];
+    __shared__ float red[2 * kTeachers / 32], total_of_p[2], extra[2][2 * kPer];
     __shared__ int flags[2];                     // 1: no entry, 2: the row fails
     __shared__ float row_high[2], row_scale[2], row_by[2];                    // of a row's gradient; by 0: it is 0
     __shared__ uint64_t full[kMaxSegments], free[kMaxSegments], told[2], done[2], joined[2];
@@ -658,9 +662,8 @@ __global__ void __launch_bounds__(kThreads + kTeachers, STEP ? 5 : 4)
 stream_kernel(const DistillArgs a, const int slots) {
     extern __shared__ __align__(128) uint4 room[];
     __shared__ Norm part[kWarps];
-    __shared__ double red64[2 * kTeachers / 32];
-    __shared__ Terms terms_of_row;
-    __shared__ float total_of_p, red[3 * kTeachers / 32];
+    __shared__ Terms red64[kTeachers / 32], terms_of_row;
+    __shared__ float total_of_p, red[2 * kTeachers / 32];
     __shared__ int flags;                        // 1: no entry, 2: the row fails
     constexpr int kPer = Slice<T>::kPer;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -762,7 +765,7 @@ stream_kernel(const DistillArgs a, const int slots) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, const int slices, const int slots) {
     extern __shared__ __align__(128) uint4 room[];
-    __shared__ float red[3 * kWarps];
+    __shared__ float red[2 * kWarps];
     constexpr int kPer = Slice<T>::kPer;
     constexpr int kAhead = 4;                    // chunks of a thread in flight
     const int t = threadIdx.x;
