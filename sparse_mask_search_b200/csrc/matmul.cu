@@ -89,7 +89,7 @@ __device__ __forceinline__ void store4(const MatmulArgs& p, int64_t r, int64_t c
 __device__ __forceinline__ void load_mask(const MatmulArgs& p, int64_t r, int64_t c, uint32_t (&w)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = p.mask && r < p.m && c + 32 * i < p.n ? __ldg(p.mask + r * p.wpr + c / 32 + i) : 0xffffffffu;
+        w[i] = p.mask && r < p.m && c + 32 * i < p.n ? p.mask[r * p.wpr + c / 32 + i] : 0xffffffffu;
 }
 __device__ __forceinline__ void apply_mask(uint32_t w, uint32_t (&v)[32]) {
 #pragma unroll

@@ -8,7 +8,9 @@ namespace tsenor {
 // The next kernel on the stream may start once every block of this one has come here.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // Waits until the kernel before this one has finished and its writes are visible.  Every thread that
-// reads or writes global memory calls it first.
+// reads or writes global memory calls it first, and reads with plain loads: a read-only load (__ldg, const
+// __restrict__) stands for memory that nothing writes while the kernel runs, which the kernel before may still do, and could be
+// moved above the wait.
 __device__ __forceinline__ void prior_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace tsenor

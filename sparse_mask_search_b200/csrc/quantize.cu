@@ -69,7 +69,7 @@ struct Eight {
     __device__ __forceinline__ void load(const typename T::storage* p) {        // 16-byte aligned
 #pragma unroll
         for (int i = 0; i < kWords; i += 4) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+            const uint4 v = reinterpret_cast<const uint4*>(p)[i / 4];
             w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
         }
     }
@@ -79,8 +79,8 @@ struct Eight {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (k < n) {
-                if constexpr (std::is_same<T, BF16>::value) w[k / 2] |= uint32_t(__ldg(p + k)) << (16 * (k & 1));
-                else w[k] = __float_as_uint(__ldg(p + k));
+                if constexpr (std::is_same<T, BF16>::value) w[k / 2] |= uint32_t(p[k]) << (16 * (k & 1));
+                else w[k] = __float_as_uint(p[k]);
             }
     }
     // The 8 entries at p, of which this thread holds the aligned words from the 16 bytes that p
@@ -94,7 +94,7 @@ struct Eight {
         uint4 n = make_uint4(__shfl_down_sync(kFullMask, w[0], 1), __shfl_down_sync(kFullMask, w[1], 1),
                              __shfl_down_sync(kFullMask, w[2], 1), __shfl_down_sync(kFullMask, w[3], 1));
         if ((threadIdx.x & 15) == 15 && valid && off)
-            n = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15)) + kWords / 4);
+            n = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15))[kWords / 4];
         uint32_t u[kWords + 4];
 #pragma unroll
         for (int i = 0; i < kWords; ++i) u[i] = w[i];
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kQThreads, sizeof(typename T::storage) == 2 ? 
 #pragma unroll
             for (int p = 0; p < kPass; ++p) {
                 bits[p] = 0u;
-                if (rl + 16 * p < rows) bits[p] = __ldg(mask + 16 * p * a.wpr * 4);
+                if (rl + 16 * p < rows) bits[p] = mask[16 * p * a.wpr * 4];
             }
         }
         if constexpr (!VEC) {
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kQThreads, sizeof(typename T::storage) == 2 ? 
         for (int p = 0; p < kPass; ++p) {
             const int n = rl + 16 * p < rows ? cols : 0;
             v[p].load_some(x + 16 * p * a.ldx, n);
-            if constexpr (MASK) bits[p] = n > 0 ? __ldg(mask + 16 * p * a.wpr * 4) : 0u;
+            if constexpr (MASK) bits[p] = n > 0 ? mask[16 * p * a.wpr * 4] : 0u;
         }
     }
     if constexpr (MASK) {                   // a masked entry is 0 whatever it held
@@ -381,8 +381,8 @@ __global__ void __launch_bounds__(kQThreads, sizeof(typename T::storage) == 2 ? 
 // power of two is exact in fp32 within its range.
 template <typename T>
 __global__ void __launch_bounds__(256)
-dequantize_kernel(const uint8_t* __restrict__ v, int64_t rows, int64_t cols, int64_t ldv,
-                  const uint8_t* __restrict__ scales, bool along_rows, typename T::storage* __restrict__ out, int64_t ldo) {
+dequantize_kernel(const uint8_t* v, int64_t rows, int64_t cols, int64_t ldv, const uint8_t* scales, bool along_rows,
+                  typename T::storage* out, int64_t ldo) {
     const int64_t per = (cols + 3) / 4;
     const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
     let_next_start();
