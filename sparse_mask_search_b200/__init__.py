@@ -424,6 +424,8 @@ def tsenor_quantize(X, block: str = "row", mask=None, out=None, stream=None):
         orows, ocols, ldv, ptr = _codes(out.values, "out.values", (torch.float8_e4m3fn,), device)
         if (orows, ocols) != (rows, cols):
             raise ValueError(f"out.values must have shape {(rows, cols)}, got {(orows, ocols)}")
+        if (code != 1 and out.scales is None) or (code != 0 and out.scales_t is None):
+            raise ValueError(f'out lacks the scales of block "{block}"')
         if code != 1:
             along = _dense(out.scales, "out.scales", torch.uint8, scale_shape(rows, cols), device)
         if code != 0:

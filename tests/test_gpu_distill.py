@@ -259,6 +259,25 @@ def test_gradient_against_differences():
     assert bool(((got - want).abs() <= third * h * h / 6 + (tol + moved) / h + 2.0 ** -20).all())
 
 
+@pytest.mark.parametrize("rows,vocab", [(18000, 131072), (500000, 5003)])
+def test_offsets_past_32_bits(rows, vocab):
+    z = torch.zeros((rows, vocab), dtype=torch.bfloat16, device="cuda")
+    tail, index, value, _ = _case(200, vocab, 10, "bf16", 16)
+    z[-200:] = tail
+    i = torch.zeros((rows, 10), dtype=torch.int32, device="cuda")
+    t = torch.zeros((rows, 10), device="cuda")
+    i[-200:], t[-200:] = index, value
+    loss, lse, grad, tol_loss, tol_grad = _reference(tail, index, value, 2.0, None, None)
+    tol_grad = tol_grad + 2.0 ** -8 * grad.abs() + torch.finfo(z.dtype).tiny
+    got, got_lse = tsl.tsenor_distill_loss(z, i, t, 2.0)
+    _near(got[-200:], loss, tol_loss)
+    _near(tsl.tsenor_distill_grad(z, i, t, got_lse, 2.0)[-200:], grad, tol_grad)
+    got, g = tsl.tsenor_distill_step(z, i, t, 2.0, grad=z)
+    _near(got[-200:], loss, tol_loss)
+    _near(g[-200:], grad, tol_grad)
+    assert tsl.tsenor_error_count() == 0
+
+
 def test_no_rows_and_no_entries():
     z = torch.randn((4, 100), device="cuda")
     none = torch.zeros((4, 0), dtype=torch.int32, device="cuda"), torch.zeros((4, 0), device="cuda")

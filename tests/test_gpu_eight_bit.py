@@ -292,6 +292,29 @@ def test_matmul_of_an_empty_sum_is_zero(form, sa, sb):
     assert tsl.tsenor_matmul(empty(0, 9), empty(7, 9)).shape == (0, 7)
 
 
+def test_offsets_past_32_bits():
+    # 70001 x 33024 entries are 2.3e9: the last rows by the large calls and by themselves
+    rows, cols = 70001, 33024
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[-300:] = _x(300, cols, "bf16", 21, False)
+    x[:-300] = 0.5
+    q = tsl.tsenor_quantize(x)
+    last = tsl.tsenor_quantize(x[-1:])
+    assert torch.equal(q.values[-1:].view(torch.uint8), last.values.view(torch.uint8))
+    assert torch.equal(_bytes(q.scales, rows, cols)[0][-1:], _bytes(last.scales, 1, cols)[0])
+    _, t = tsl.tsenor_quantize_pair(x[:, :130])
+    _check_quantized(t, x[:, :130], "column")
+    del x
+    w = tsl.tsenor_quantize(_x(130, cols, "f32", 22, False), "tile")
+    want, size = _product(tsl.QuantizedMatrix(last.values, last.scales), w, "nt")
+    _check_product(tsl.tsenor_matmul(q, w, dtype=torch.float32)[-1:], want, size, cols)
+    # an output of 70001 x 33024
+    a, b = tsl.tsenor_quantize(_x(rows, 130, "f32", 23, False)), tsl.tsenor_quantize(_x(cols, 130, "f32", 24, False))
+    out = tsl.tsenor_matmul(a, b)
+    va, vb = _values(a, False)[-2:], _values(b, False)
+    _check_product(out[-2:], va @ vb.t(), va.abs() @ vb.abs().t(), 130)
+
+
 def test_binding_refusals():
     x = _x(16, 64, "bf16", 1, False)
     q = tsl.tsenor_quantize(x)
@@ -299,6 +322,8 @@ def test_binding_refusals():
         tsl.tsenor_quantize(x.half())
     with pytest.raises(ValueError):
         tsl.tsenor_quantize(x.t())
+    with pytest.raises(ValueError):
+        tsl.tsenor_quantize(x, "tile", out=q)                           # no scales_t to write
     with pytest.raises(ValueError):
         tsl.tsenor_quantize(x, "row", mask=torch.zeros((16, 3), dtype=torch.int32, device="cuda"))
     with pytest.raises(TypeError):
