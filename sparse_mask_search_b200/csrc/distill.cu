@@ -655,15 +655,15 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
 }
 
 // The same with one CTA to a row, which streams it through registers, twice for the step
-// (the second time from L2, last chunks first).  Nothing of a row waits for another SM, and a row's fixed costs
+// (the second time from L2, last chunks first).  W threads take the row, E its entries.  Nothing of a row waits for another SM, and a row's fixed costs
 // are paid once.
-template <typename T, bool STEP>
-__global__ void __launch_bounds__(kThreads + kTeachers, STEP ? 5 : 4)
+template <typename T, bool STEP, int W, int E>
+__global__ void __launch_bounds__(W + E, (STEP ? 1920 : 1536) / (W + E))
 stream_kernel(const DistillArgs a, const int slots) {
     extern __shared__ __align__(128) uint4 room[];
-    __shared__ Norm part[kWarps];
-    __shared__ Terms red64[kTeachers / 32], terms_of_row;
-    __shared__ float total_of_p, red[2 * kTeachers / 32];
+    __shared__ Norm part[W / 32];
+    __shared__ Terms red64[E / 32], terms_of_row;
+    __shared__ float total_of_p, red[2 * E / 32];
     __shared__ int flags;                        // 1: no entry, 2: the row fails
     constexpr int kPer = Slice<T>::kPer;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -671,24 +671,24 @@ stream_kernel(const DistillArgs a, const int slots) {
     const auto* z = static_cast<const typename T::storage*>(a.logits) + row * a.ld;
     auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
     const Slice<T> slice(z, int(a.vocab), 0, 1);
-    using Extra = Team<kThreads, kTeachers, 1>;
-    Teacher<Extra, kTeachers> teacher(room, reinterpret_cast<int*>(room) + (a.top + 3) / 4 * 4 * 3, a.top, slots);
+    using Extra = Team<W, E, 1>;
+    Teacher<Extra, E> teacher(room, reinterpret_cast<int*>(room) + (a.top + 3) / 4 * 4 * 3, a.top, slots);
     const bool vec = STEP && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     const float inv_t = 1.f / a.temperature, scale2 = inv_t * kLog2E;
     const uint4* in = reinterpret_cast<const uint4*>(z + slice.first);
     let_next_start();
     prior_done();
-    if (warp >= kWarps) {
+    if (warp >= W / 32) {
         bool empty, bad;
         teacher.read_entries(a, row, &empty, &bad);
-        if (t == kThreads) flags = (empty ? 1 : 0) | (bad ? 2 : 0);
+        if (t == W) flags = (empty ? 1 : 0) | (bad ? 2 : 0);
         if (STEP) __syncthreads();
         if (!empty && !(STEP && bad)) {
             if (STEP) teacher.mark_twins(slice);
             double c;
             const float total = teacher.weights(a, row, red, &c);
             const Terms terms = team_terms<T>(a, z, slice, teacher, c, red64);
-            if (t == kThreads) {
+            if (t == W) {
                 total_of_p = total;
                 terms_of_row = terms;
             }
@@ -699,13 +699,13 @@ stream_kernel(const DistillArgs a, const int slots) {
             // a NaN or +inf anywhere makes the sum NaN
             Norm norm{-INFINITY, 0.f};
             int c = t;
-            for (; c + (kGroup - 1) * kThreads < slice.chunks; c += kGroup * kThreads) {
+            for (; c + (kGroup - 1) * W < slice.chunks; c += kGroup * W) {
                 uint4 v[kGroup];
 #pragma unroll
-                for (int k = 0; k < kGroup; ++k) v[k] = in[c + k * kThreads];
+                for (int k = 0; k < kGroup; ++k) v[k] = in[c + k * W];
                 take<T, kGroup>(norm, v, scale2);
             }
-            for (; c < slice.chunks; c += kThreads) {
+            for (; c < slice.chunks; c += W) {
                 const uint4 v = in[c];
                 take<T, 1>(norm, &v, scale2);
             }
@@ -718,21 +718,21 @@ stream_kernel(const DistillArgs a, const int slots) {
     const bool empty = flags & 1;
     bool failed = flags & 2;
     if (STEP && flags) {
-        if (warp < kWarps) write_zeros<T, kThreads>(g, slice, vec);
+        if (warp < W / 32) write_zeros<T, W>(g, slice, vec);
         if (t == 0) {
             a.loss[row] = failed ? NAN : 0.f;
             if (failed) atomicAdd(&g_row_failures, 1ull);
         }
         return;
     }
-    const Norm norm = join(kWarps, scale2, [&](int k) { return part[k]; });
+    const Norm norm = join(W / 32, scale2, [&](int k) { return part[k]; });
     const float m = norm.high;
     failed = failed || (!empty && !(fabsf(m) < INFINITY && norm.sum < INFINITY));
-    if (t == kThreads) write_loss<STEP>(a, row, norm, empty ? Terms{0.0, 0.0} : terms_of_row, empty, failed);
+    if (t == W) write_loss<STEP>(a, row, norm, empty ? Terms{0.0, 0.0} : terms_of_row, empty, failed);
     if constexpr (STEP) {
         const float by = a.temperature * (a.weight ? a.weight[row] : 1.f);
         if (failed || by == 0.f) {
-            if (warp < kWarps) write_zeros<T, kThreads>(g, slice, vec);
+            if (warp < W / 32) write_zeros<T, W>(g, slice, vec);
             return;
         }
         const float scale = by * total_of_p / norm.sum;
@@ -742,22 +742,22 @@ stream_kernel(const DistillArgs a, const int slots) {
             x = mul2(add2(x, minus_m), by2);
             return mul2(make_float2(ex2(x.x), ex2(x.y)), scale_2);
         };
-        if (warp < kWarps) {
+        if (warp < W / 32) {
             int c = slice.chunks - 1 - t;
-            for (; c - (kGroup - 1) * kThreads >= 0; c -= kGroup * kThreads) {
+            for (; c - (kGroup - 1) * W >= 0; c -= kGroup * W) {
                 uint4 v[kGroup];
 #pragma unroll
-                for (int k = 0; k < kGroup; ++k) v[k] = in[c - k * kThreads];
+                for (int k = 0; k < kGroup; ++k) v[k] = in[c - k * W];
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k)
-                    write_chunk<T>(g + slice.first + (c - k * kThreads) * kPer, v[k], vec, both);
+                    write_chunk<T>(g + slice.first + (c - k * W) * kPer, v[k], vec, both);
             }
-            for (; c >= 0; c -= kThreads) write_chunk<T>(g + slice.first + c * kPer, in[c], vec, both);
+            for (; c >= 0; c -= W) write_chunk<T>(g + slice.first + c * kPer, in[c], vec, both);
             if (t < slice.extras()) write<T>(g + slice.extra(t), at(read<T>(z + slice.extra(t))));
         }
         __syncthreads();                         // the entries' columns are written again
-        if (warp < kWarps)
-            teacher.template each<kThreads>(t, slice, [&](int j, int v, float w) { write<T>(g + v, at(teacher.logit[j]) - by * w); });
+        if (warp < W / 32)
+            teacher.template each<W>(t, slice, [&](int j, int v, float w) { write<T>(g + v, at(teacher.logit[j]) - by * w); });
     }
 }
 
@@ -833,16 +833,29 @@ int slices_of(int64_t rows, int64_t row_bytes) {
 
 // Streaming pays where a row's fixed costs weigh more than a second read: for the loss
 // (which has none) wherever the rows fill the device, 93 us against 139 for 2048 x 131072 bf16; for the step with
-// short rows, 36 us against 57 for 4096 x 1000 and 13 against 18 for 512 x 10000, but 65 against 58 for
+// short rows, 18 us against 57 for 4096 x 1000 and 11 against 18 for 512 x 10000, but 65 against 58 for
 // 2048 x 32000.
-bool streams(bool step, int64_t rows, int64_t row_bytes) { return rows >= 148 && (!step || row_bytes <= 32 * 1024); }
+constexpr int64_t kShortRow = 32 * 1024;
+bool streams(bool step, int64_t rows, int64_t row_bytes) { return rows >= 148 && (!step || row_bytes <= kShortRow); }
+
+// Threads of a streaming CTA: on the row, and on its entries.  Short rows wait for the entries, so that where
+// there are more rows than the wide CTAs that run at once, smaller ones, more to an SM, pay: with 64 entries 18 us
+// for a step of 4096 x 1000 bf16 against 33, 13 against 24 for its loss, 19 against 29 for the loss of 4096 x 8000.
+// Long rows want the loads of a wide CTA (the loss of 2048 x 131072 takes 93 us and would take 108), many entries
+// its threads (1000 of them, 512 x 2000: 21 and would take 29).
+constexpr int kNarrow = 96, kNarrowTeachers = 64;
+
+template <typename T, bool STEP, int W, int E>
+cudaError_t launch_stream(const DistillArgs& a, cudaStream_t st) {
+    return launch_early(stream_kernel<T, STEP, W, E>, a.rows, W + E, teacher_bytes(a.top, 1), 1, st, a, slots_of(a.top));
+}
 
 template <typename T, bool STEP>
 cudaError_t launch_loss(const DistillArgs& a, cudaStream_t st) {
     const int64_t row_bytes = a.vocab * int64_t(sizeof(typename T::storage));
     if (streams(STEP, a.rows, row_bytes)) {
-        return launch_early(stream_kernel<T, STEP>, a.rows, kThreads + kTeachers, teacher_bytes(a.top, 1), 1, st, a,
-                            slots_of(a.top));
+        return row_bytes <= kShortRow && a.rows > 4 * 148 ? launch_stream<T, STEP, kNarrow, kNarrowTeachers>(a, st)
+                                                          : launch_stream<T, STEP, kThreads, kTeachers>(a, st);
     }
     const int slices = slices_of(a.rows, row_bytes);
     const int chunk_room = int((row_bytes / 16 + slices - 1) / slices);
