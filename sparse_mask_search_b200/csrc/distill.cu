@@ -655,8 +655,8 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
 }
 
 // The same with one CTA to a row, which streams it through registers, twice for the step
-// (the second time from L2, last chunks first).  W threads take the row, E its entries.  Nothing of a row waits for another SM, and a row's fixed costs
-// are paid once.
+// (the second time from L2, last chunks first).  W threads take the row, E its entries.  Nothing of a row waits for
+// another SM, and a row's fixed costs are paid once.
 template <typename T, bool STEP, int W, int E>
 __global__ void __launch_bounds__(W + E, (STEP ? 1920 : 1536) / (W + E))
 stream_kernel(const DistillArgs a, const int slots) {

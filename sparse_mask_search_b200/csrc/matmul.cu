@@ -6,8 +6,8 @@
 // contracted axis; the same byte for four such steps): sums stay in tensor memory in fp32 from the first block to
 // the last and are rounded once.  Codes stored along either axis are read as they are, K-major or MN-major.
 // Bound by the tensor cores (and, on random data, by the card's power limit) for many rows, by the bytes
-// of B for few.  Measured, with the host's share: 4096 x 28672 x 8192 nt 764 us (2.52 PFLOP/s; 486 us on zeros, where
-// the clock stays at 1965 MHz), 2048 x 11008 x 4096 84 us, 1 x 11008 x 4096 12.3 us (3.7 TB/s).
+// of B for few.  Measured, with the host's share: 4096 x 28672 x 8192 nt 744 us (2.59 PFLOP/s; 486 us on zeros, where
+// the clock stays at 1965 MHz), 2048 x 11008 x 4096 82 us, 1 x 11008 x 4096 12.3 us (3.7 TB/s).
 #include <mutex>
 
 #include <cudaTypedefs.h>
