@@ -6,13 +6,15 @@
 //   loss = T^2 sum_j p_j (log p_j - log q_{i_j})
 //   dz_v = w T (P q_v - sum_{j: i_j = v} p_j),  P = sum_j p_j
 //
-// Bound by memory: z is read once and dz written once.  For the loss, a row is
-// cut into slices of at most 64 KB, one to a CTA of a cluster of up to 8; bulk
-// copies bring the slice into shared memory, where its maximum, its sum of
-// exponentials and, for the step, its gradient are taken, and the CTAs exchange one
-// (maximum, sum, loss term) each.  Three CTAs to an SM overlap one row's loads with
-// another's arithmetic and stores.  A few rows get more and smaller slices.  The
-// gradient alone needs nothing but z and lse: it streams through registers, as does the loss of many rows.
+// Bound by memory: z is read once and dz written once.  Three kernels:
+//   stream_kernel  a row to a CTA, through registers: the loss of many rows, and the step, which reads a row again
+//                  from L2, of many rows of up to 192 KB.
+//   loss_kernel    a row cut into slices of at most 64 KB, one to a CTA of a cluster of up to 8: few rows, and the step
+//                  of longer ones.  Bulk copies bring the slice into shared memory, where its maximum, its sum of
+//                  exponentials and, for the step, its gradient are taken, and the CTAs exchange one (maximum, sum,
+//                  loss term) each.  Three CTAs to an SM overlap one row's loads with another's arithmetic and
+//                  stores.  A few rows get more and smaller slices.
+//   grad_kernel    the gradient alone, which needs nothing but z and lse.
 // Sums over the vocabulary are fp32, the few scalars of a row fp64.  Measured at 2048 x 131072 bf16, 64 entries: loss 93 us
 // (5.8 TB/s), step 227 us (4.7 TB/s), gradient 175 us (6.1 TB/s).
 #include <type_traits>
@@ -286,14 +288,15 @@ __device__ void write_zeros(typename T::storage* g, const Slice<T>& slice, bool 
     for (int i = threadIdx.x; i < slice.extras(); i += M) write<T>(g + slice.extra(i), 0.f);
 }
 
-// One chunk of gradient from f(logit) of its entries.
-template <typename T, typename F>
+// One chunk of gradient from f(logit) of its entries.  LAST: it should not push from L2 what will be read again.
+template <typename T, bool LAST = false, typename F>
 __device__ __forceinline__ void write_chunk(typename T::storage* g, const uint4& z, bool vec, F f) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < Slice<T>::kPer / 2; ++i) set_pair<T>(w, i, f(pair_of<T>(z, i)));
     if (vec) {
-        *reinterpret_cast<uint4*>(g) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (LAST) __stcs(reinterpret_cast<uint4*>(g), make_uint4(w[0], w[1], w[2], w[3]));
+        else *reinterpret_cast<uint4*>(g) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
         for (int k = 0; k < Slice<T>::kPer; ++k) {
@@ -747,12 +750,12 @@ stream_kernel(const DistillArgs a, const int slots) {
             for (; c - (kGroup - 1) * W >= 0; c -= kGroup * W) {
                 uint4 v[kGroup];
 #pragma unroll
-                for (int k = 0; k < kGroup; ++k) v[k] = in[c - k * W];
+                for (int k = 0; k < kGroup; ++k) v[k] = __ldcs(in + c - k * W);
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k)
-                    write_chunk<T>(g + slice.first + (c - k * W) * kPer, v[k], vec, both);
+                    write_chunk<T, true>(g + slice.first + (c - k * W) * kPer, v[k], vec, both);
             }
-            for (; c >= 0; c -= W) write_chunk<T>(g + slice.first + c * kPer, in[c], vec, both);
+            for (; c >= 0; c -= W) write_chunk<T, true>(g + slice.first + c * kPer, __ldcs(in + c), vec, both);
             if (t < slice.extras()) write<T>(g + slice.extra(t), at(read<T>(z + slice.extra(t))));
         }
         __syncthreads();                         // the entries' columns are written again
@@ -832,17 +835,19 @@ int slices_of(int64_t rows, int64_t row_bytes) {
 }
 
 // Streaming pays where a row's fixed costs weigh more than a second read: for the loss
-// (which has none) wherever the rows fill the device, 93 us against 139 for 2048 x 131072 bf16; for the step with
-// short rows, 18 us against 57 for 4096 x 1000 and 11 against 18 for 512 x 10000, but 65 against 58 for
-// 2048 x 32000.
-constexpr int64_t kShortRow = 32 * 1024;
-bool streams(bool step, int64_t rows, int64_t row_bytes) { return rows >= 148 && (!step || row_bytes <= kShortRow); }
+// (which has none) wherever the rows fill the device, 93 us against 139 for 2048 x 131072 bf16; for the step as long as
+// the rows in work stay in L2, five to an SM, which second reads and stores marked as the last use help: 18 us
+// against 57 for 4096 x 1000 bf16, 58 against 62 for 2048 x 32000, 148 against 182 for 2048 x 80000, 142 against 155
+// for 2048 x 40000 fp32, but 182 against 175 for 2048 x 50000 fp32 and 243 against 236 for 2048 x 131072 bf16.
+constexpr int64_t kStepRow = 192 * 1024;
+bool streams(bool step, int64_t rows, int64_t row_bytes) { return rows >= 148 && (!step || row_bytes <= kStepRow); }
 
 // Threads of a streaming CTA: on the row, and on its entries.  Short rows wait for the entries, so that where
 // there are more rows than the wide CTAs that run at once, smaller ones, more to an SM, pay: with 64 entries 18 us
 // for a step of 4096 x 1000 bf16 against 33, 13 against 24 for its loss, 19 against 29 for the loss of 4096 x 8000.
 // Long rows want the loads of a wide CTA (the loss of 2048 x 131072 takes 93 us and would take 108), many entries
 // its threads (1000 of them, 512 x 2000: 21 and would take 29).
+constexpr int64_t kShortRow = 32 * 1024;
 constexpr int kNarrow = 96, kNarrowTeachers = 64;
 
 template <typename T, bool STEP, int W, int E>

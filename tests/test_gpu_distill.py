@@ -189,7 +189,8 @@ def test_strided_rows_and_the_gradient_in_place(dtype, rows, vocab):
 
 
 @pytest.mark.parametrize("dtype,rows,vocab", [("bf16", 600, 33000), ("bf16", 450, 60001), ("f32", 120, 131072), ("f32", 150, 262143),
-                                              ("bf16", 700, 5003), ("f32", 900, 4099), ("bf16", 450, 5003), ("bf16", 147, 200001)])
+                                              ("f32", 147, 65003), ("bf16", 500, 110001), ("bf16", 700, 5003),
+                                              ("f32", 900, 4099), ("bf16", 450, 5003), ("bf16", 147, 200001)])
 @pytest.mark.parametrize("top", [9, 200])
 def test_many_rows_of_every_kind(dtype, rows, vocab, top):
     # blocks that walk several rows: with and without entries, failing, without weight, in any order
@@ -219,7 +220,7 @@ def test_many_rows_of_every_kind(dtype, rows, vocab, top):
     tsl.tsenor_error_count()
 
 
-@pytest.mark.parametrize("dtype,rows,vocab", [("bf16", 500, 33000), ("f32", 100, 131072)])
+@pytest.mark.parametrize("dtype,rows,vocab", [("bf16", 500, 33000), ("bf16", 800, 5003), ("f32", 100, 131072)])
 def test_captured_and_replayed(dtype, rows, vocab):
     first, second = (_case(rows, vocab, 20, dtype, s)[:3] for s in (14, 15))
     want = []
