@@ -368,7 +368,8 @@ tsenor_status tsenor_matmul(tsenor_form form, const uint8_t* a, int64_t lda, con
  *   weight:     rows fp32, or NULL for 1: the loss's upstream gradient, 0 for
  *               a token that does not count.
  * A row without entries (a prompt or padding token) has loss 0 and gradient 0,
- * whatever its logits hold.  A row that has entries and an index of vocab or
+ * whatever its logits hold; its lse is that of its logits (+inf with a +inf
+ * among them, NaN with a NaN, -inf without any above -inf).  A row that has entries and an index of vocab or
  * more, a teacher value that is NaN or +inf, a NaN or +inf among its logits, or
  * no finite logit fails: its loss (and lse) is NaN, its gradient 0, and it is
  * added to the counter of tsenor_error_count.  The other rows are unaffected.

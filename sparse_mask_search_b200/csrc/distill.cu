@@ -17,6 +17,7 @@
 //   grad_kernel    the gradient alone, which needs nothing but z and lse.
 // Sums over the vocabulary are fp32, the few scalars of a row fp64.  Measured at 2048 x 131072 bf16, 64 entries: loss 93 us
 // (5.8 TB/s), step 227 us (4.7 TB/s), gradient 175 us (6.1 TB/s).
+#include <cfloat>
 #include <type_traits>
 
 #include "common.cuh"
@@ -151,8 +152,9 @@ struct Plus {
     __device__ X operator()(X a, X b) const { return a + b; }
 };
 
-// log of a sum of 1 or more in fp64: the exponent apart, so that logf sees [1, 2).
+// log of a sum of 1 or more in fp64: the exponent apart, so that logf sees [1, 2). What is not finite is its own log.
 __device__ __forceinline__ double log_sum(float s) {
+    if (!(s < INFINITY)) return s;
     const int e = int(__float_as_uint(s) >> 23) - 127;
     return double(e) * 0.6931471805599453 + double(logf(__uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u)));
 }
@@ -306,12 +308,13 @@ __device__ __forceinline__ void write_chunk(typename T::storage* g, const uint4&
     }
 }
 
-// A softmax normaliser in units of z: sum of 2^((z - high) scale).  A part without a
-// finite logit has high -inf and sum 0, or NaN if it holds one; both survive the joins.
+// A softmax normaliser in units of z: sum of 2^((z - high) scale), where `high` counts as the nearest finite
+// value.  A part without a finite logit has high -inf and sum 0; a +inf makes the sum +inf, a NaN anywhere makes
+// it NaN.  All of it survives the joins.
 struct Norm {
     float high, sum;
 };
-__device__ __forceinline__ float finite_base(float high) { return high == -INFINITY ? 0.f : high; }
+__device__ __forceinline__ float finite_base(float high) { return fminf(fmaxf(high, -FLT_MAX), FLT_MAX); }
 // `n` normalisers, read through get(k).
 template <typename F>
 __device__ __forceinline__ Norm join(int n, float scale2, F get) {
@@ -548,7 +551,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar);
             };
-            // one pass over the slice; a NaN or +inf anywhere makes the sum NaN
+            // one pass over the slice; a NaN or +inf anywhere makes the sum one too
             Norm norm{-INFINITY, 0.f};
             for (int s = 0; s < segments; ++s) {
                 if (!mbar_sleep_bounded(full + s, i & 1)) { stalled = true; break; }
@@ -699,7 +702,7 @@ stream_kernel(const DistillArgs a, const int slots) {
     } else {
         if (STEP) __syncthreads();
         if (!(STEP && flags)) {
-            // a NaN or +inf anywhere makes the sum NaN
+            // a NaN or +inf anywhere makes the sum one too
             Norm norm{-INFINITY, 0.f};
             int c = t;
             for (; c + (kGroup - 1) * W < slice.chunks; c += kGroup * W) {
