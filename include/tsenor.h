@@ -376,7 +376,12 @@ tsenor_status tsenor_matmul(tsenor_form form, const uint8_t* a, int64_t lda, con
  *
  * tsenor_distill_loss:  loss and lse (for tsenor_distill_grad).
  * tsenor_distill_step:  loss and gradient from one read of the logits.
- * tsenor_distill_grad:  the gradient from lse, which the same logits gave.
+ * tsenor_distill_grad:  the gradient from lse, which the same logits gave.  A
+ * rounded lse is off by 2^-24 of itself, and so is every q relative to its
+ * value: rows of |lse| above 64 (low temperatures, logits far from 0) get their
+ * normaliser anew from one more read, by one block to a row.  The logits of
+ * those rows decide whether they fail, those of other rows are not looked at
+ * again.  A NaN lse fails.
  * grad has the type of the logits, ldg elements from row to row; it may be
  * the logits' own memory (same pointer, ldg == ld).  The sums are fp32 in a
  * fixed order: the same call gives the same bits.  TSENOR_ERR_SHAPE for top,

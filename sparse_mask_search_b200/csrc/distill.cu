@@ -767,11 +767,39 @@ stream_kernel(const DistillArgs a, const int slots) {
     }
 }
 
+// A whole row's normaliser by the threads of a block, in every thread.
+template <typename T>
+__device__ Norm block_norm(const typename T::storage* z, const Slice<T>& row, float scale2, Norm* part) {
+    const uint4* in = reinterpret_cast<const uint4*>(z + row.first);
+    Norm norm{-INFINITY, 0.f};
+    int c = threadIdx.x;
+    for (; c + (kGroup - 1) * kThreads < row.chunks; c += kGroup * kThreads) {
+        uint4 v[kGroup];
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) v[k] = in[c + k * kThreads];
+        take<T, kGroup>(norm, v, scale2);
+    }
+    for (; c < row.chunks; c += kThreads) {
+        const uint4 v = in[c];
+        take<T, 1>(norm, &v, scale2);
+    }
+    if (threadIdx.x < row.extras()) take_one(norm, read<T>(z + row.extra(threadIdx.x)), scale2);
+    norm = warp_join(norm, scale2);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = norm;
+    __syncthreads();
+    return join(kWarps, scale2, [&](int k) { return part[k]; });
+}
+
 // The gradient from lse; blockIdx.x is a row's slice.
+// q = exp(z / T - lse) as unit * 2^((z - base) log2(e) / T): base = T lse in fp32, what its rounding leaves in `unit`, so that the
+// error of q is that of lse itself, 2^-24 |lse|, and some 2^-22.  A larger lse (low temperatures, logits far from 0) or a T lse past
+// fp32 is not used: the row's first block takes the row by itself, maximum and sum anew from one more read, as the step has them.
+constexpr float kNearLse = 64.f;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, const int slices, const int slots) {
     extern __shared__ __align__(128) uint4 room[];
     __shared__ float red[2 * kWarps];
+    __shared__ Norm part[kWarps];
     constexpr int kPer = Slice<T>::kPer;
     constexpr int kAhead = 4;                    // chunks of a thread in flight
     const int t = threadIdx.x;
@@ -779,17 +807,27 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     const int rank = int(blockIdx.x % slices);
     const auto* z = static_cast<const typename T::storage*>(a.logits) + row * a.ld;
     auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
-    const Slice<T> slice(z, int(a.vocab), rank, slices);
+    Slice<T> slice(z, int(a.vocab), rank, slices);
     Teacher<Team<0, kThreads, 1>, kThreads> teacher(room, reinterpret_cast<int*>(room) + (a.top + 3) / 4 * 4 * 3, a.top, slots);
     float* target = teacher.logit;               // the gradients of the entries' columns
     const bool vec = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     let_next_start();
     prior_done();
-    const float lse = a.lse[row];
+    const float lse = a.lse[row], scale2 = 1.f / a.temperature * kLog2E;
+    const double middle = double(lse) * double(a.temperature);
     const float by = a.temperature * (a.weight ? a.weight[row] : 1.f);
+    float base = float(middle), unit = expf(float((double(base) - middle) * a.inv_t));
     bool empty, bad;
     teacher.read_entries(a, row, &empty, &bad);
-    bad = bad || (!empty && !(fabsf(lse) < INFINITY));
+    bad = bad || (!empty && lse != lse);
+    if (!bad && !empty && !(fabsf(lse) <= kNearLse && fabsf(base) <= FLT_MAX)) {
+        if (rank > 0) return;
+        slice = Slice<T>(z, int(a.vocab), 0, 1);
+        const Norm norm = block_norm<T>(z, slice, scale2, part);
+        bad = !(fabsf(norm.high) < INFINITY && norm.sum < INFINITY);
+        base = norm.high;
+        unit = 1.f / norm.sum;
+    }
     if (bad && rank == 0 && t == 0) atomicAdd(&g_row_failures, 1ull);
     if (bad || empty || by == 0.f) {
         write_zeros<T, kThreads>(g, slice, vec);
@@ -807,20 +845,19 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     double c;
     const float total = teacher.weights(a, row, red, &c);
     __syncthreads();
-    const float inv_t = 1.f / a.temperature, scale = by * total;
-    auto at = [&](float x) { return scale * ex2(fmaf(x, inv_t, -lse) * kLog2E); };
+    const float scale = by * total * unit;
+    auto at = [&](float x) { return scale * ex2((x - base) * scale2); };
     // the entries' gradients before anything is written: grad may be the logits
     teacher.template each<kThreads>(t, slice, [&](int j, int c, float w) { target[j] = at(read<T>(z + c)) - by * w; });
     __syncthreads();
-    const float2 inv2 = make_float2(inv_t, inv_t), minus = make_float2(-lse, -lse), l2 = make_float2(kLog2E, kLog2E),
-                 scale_2 = make_float2(scale, scale);
+    const float2 minus = make_float2(-base, -base), by2 = make_float2(scale2, scale2), scale_2 = make_float2(scale, scale);
     for (int c = t; c < slice.chunks; c += kAhead * kThreads) {
         if (c != t) load(c);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             if (c + i * kThreads < slice.chunks)
                 write_chunk<T>(g + slice.first + (c + i * kThreads) * kPer, v[i], vec, [&](float2 x) {
-                    x = mul2(fma2(x, inv2, minus), l2);
+                    x = mul2(add2(x, minus), by2);
                     return mul2(make_float2(ex2(x.x), ex2(x.y)), scale_2);
                 });
     }
