@@ -15,6 +15,15 @@ tsenor_status cuda_fail(cudaError_t e, const char* what);
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// encode(), a call of the driver's tensor map encoder: it wants a context, which a host thread has only once it has called the
+// runtime, so that the first call of a thread may have to make it and try again.
+template <typename F>
+cudaError_t with_context(F encode) {
+    CUresult r = encode();
+    if (r != CUDA_SUCCESS && cudaFree(nullptr) == cudaSuccess) r = encode();
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // Launches a kernel whose threads call prior_done() (pdl.h) before they touch global memory: it may start,
 // and set itself up, while the kernel before it on the stream still runs.  cluster: CTAs
 // of a cluster, 1 for none.

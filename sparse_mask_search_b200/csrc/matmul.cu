@@ -579,9 +579,10 @@ cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, const void* v, ui
     const cuuint64_t dims[2] = {inner, outer};               // what lies past the matrix reads as 0
     const cuuint64_t strides[1] = {stride};
     const cuuint32_t box[2] = {box_inner, box_outer}, estr[2] = {1, 1};
-    const CUresult r = g_encode(map, type, 2, const_cast<void*>(v), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    return with_context([&] {
+        return g_encode(map, type, 2, const_cast<void*>(v), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 // The codes of an operand whose tiles have `own` of its uncontracted and 128 of the

@@ -65,10 +65,11 @@ cudaError_t encode_w_map(CUtensorMap* map, const void* W, int64_t rows, int64_t 
     const cuuint32_t estr[2] = {1, 1};
     const CUtensorMapDataType dt = std::is_same<T, BF16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    const CUresult r = g_encode_tiled(map, dt, 2, const_cast<void*>(W), dims, strides, box, estr,
-                                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    return with_context([&] {
+        return g_encode_tiled(map, dt, 2, const_cast<void*>(W), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 template <int M, typename T, bool EXT>
