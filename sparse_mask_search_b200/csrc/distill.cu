@@ -270,13 +270,13 @@ struct Teacher {
     }
 };
 
-int slots_of(int top) {
+constexpr int slots_of(int top) {
     int n = 32;
     while (n < 2 * top) n *= 2;
     return n;
 }
 // Shared memory of `rows` rows' entries and a table.
-unsigned teacher_bytes(int top, int rows) { return unsigned(rows * ((top + 3) / 4 * 4) * 12 + slots_of(top) * 4); }
+constexpr unsigned teacher_bytes(int top, int rows) { return unsigned(rows * ((top + 3) / 4 * 4) * 12 + slots_of(top) * 4); }
 
 // Gradient 0 for the columns of a slice.
 template <typename T, int M>
@@ -905,7 +905,9 @@ cudaError_t launch_loss(const DistillArgs& a, cudaStream_t st) {
     const int slices = slices_of(a.rows, row_bytes);
     const int chunk_room = int((row_bytes / 16 + slices - 1) / slices);
     const unsigned bytes = unsigned(chunk_room * 16) + teacher_bytes(a.top, 2);
-    cudaError_t e = cudaFuncSetAttribute(loss_kernel<T, STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    constexpr unsigned most = kMaxSegments * kSegment * 16 + teacher_bytes(kMaxTop, 2);
+    static_assert(most + 4096 <= 227 * 1024, "shared memory of a CTA");
+    cudaError_t e = allow_shared(loss_kernel<T, STEP>, most);
     if (e != cudaSuccess) return e;
     // No more clusters than run at once, or the last ones would start when the others are through.
     int64_t clusters = a.rows;

@@ -45,6 +45,13 @@ cudaError_t launch_early(void (*kernel)(P...), int64_t grid, int block, size_t s
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// Lets launches of a kernel on the current device ask for up to `most` bytes of dynamic shared memory.  The limit belongs to
+// the kernel, which all host threads share: `most` is a constant of the kernel, never what one launch needs.
+template <typename... P>
+cudaError_t allow_shared(void (*kernel)(P...), unsigned most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
+}
+
 // How many clusters of a kernel the current device runs at once.
 template <typename... P>
 cudaError_t clusters_that_fit(int* count, void (*kernel)(P...), int block, size_t smem, int cluster) {

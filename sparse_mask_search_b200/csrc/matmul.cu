@@ -191,6 +191,9 @@ struct TileSmem {
     }
     __host__ __device__ unsigned bytes(int stages) const { return bars + (2 * stages + 4) * 8 + 16; }
 };
+// The most that a launch asks for: the smallest stage (8 rows of A) gives 12 stages at most.
+constexpr unsigned kTileMost = kStageBytes + (2 * (kStageBytes / (9 * 1024 * 2)) + 4) * 8 + 16 + 1024;
+static_assert(kTileMost <= 227 * 1024, "shared memory of a CTA");
 
 template <bool SPLIT, bool BF16OUT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -613,7 +616,7 @@ cudaError_t launch_pair(MatmulArgs p, const uint8_t* a, int64_t lda, const uint8
     constexpr unsigned bytes = PairSmem::bytes + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     auto* kernel = p.bf16 ? pair_kernel<true> : pair_kernel<false>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    e = allow_shared(kernel, bytes);
     if (e != cudaSuccess) return e;
     return launch_early(kernel, grid, kPairThreads, bytes, 2, st, map_a, map_b, map_sa, map_sb, p);
 }
@@ -633,7 +636,7 @@ cudaError_t launch_tiles(MatmulArgs p, const uint8_t* a, int64_t lda, const uint
     p.stages = (kStageBytes - 4 * 32 * 33 * 4) / (p.a_bytes + kTileBytes + 2 * kScaleBytes);
     const unsigned bytes = TileSmem(p.stages, p.a_bytes).bytes(p.stages) + 1024;
     auto* kernel = p.bf16 ? tile_kernel<SPLIT, true> : tile_kernel<SPLIT, false>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    e = allow_shared(kernel, kTileMost);
     if (e != cudaSuccess) return e;
     const int64_t tiles = p.tiles_m * p.tiles_n;
     return launch_early(kernel, SPLIT ? tiles * split : tiles < kSms ? tiles : kSms, kThreads, bytes, split, st, map_a, map_b, p,

@@ -35,3 +35,57 @@ def test_the_first_call_of_a_host_thread(call):
     torch.cuda.synchronize()
     assert not errors, errors
     assert torch.equal(got[0], want)
+
+
+def _product(m):
+    g = torch.Generator(device="cuda").manual_seed(m)
+    a = tsl.tsenor_quantize(torch.randn((m, 2048), generator=g, device="cuda"))
+    b = tsl.tsenor_quantize(torch.randn((256, 2048), generator=g, device="cuda"))
+    out, stream = torch.empty((m, 256), device="cuda"), torch.cuda.Stream()
+    args = (tsl.FORMS["nt"], a.values.data_ptr(), 2048, a.scales.data_ptr(), b.values.data_ptr(), 2048, b.scales.data_ptr(),
+            m, 256, 2048, None, out.data_ptr(), tsl.TSENOR_F32, 256, stream.cuda_stream)
+    return tsl.lib().tsenor_matmul, args, out, (a, b, stream)
+
+
+def _step(rows, vocab, top):
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    z = torch.randn((rows, vocab), generator=g, device="cuda")
+    value, index = z.topk(top, 1)
+    index, value, out = index.to(torch.int32), value.contiguous(), torch.empty_like(z)
+    loss, stream = torch.empty((rows,), device="cuda"), torch.cuda.Stream()
+    args = (z.data_ptr(), tsl.TSENOR_F32, rows, vocab, vocab, index.data_ptr(), value.data_ptr(), top, None, 2.0, None,
+            loss.data_ptr(), out.data_ptr(), vocab, stream.cuda_stream)
+    return tsl.lib().tsenor_distill_step, args, out, (z, index, value, loss, stream)
+
+
+@pytest.mark.parametrize("make,sizes", [(_product, [(64,), (8,), (128,)]), (_step, [(2, 262144, 500), (3, 1000, 4)])],
+                         ids=["products", "distillation"])
+def test_calls_of_different_sizes_from_several_threads(make, sizes):
+    # what a launch asks for (its shared memory) belongs to the launch, not to the kernel that the threads share
+    jobs = [make(*s) for s in sizes]
+    torch.cuda.synchronize()
+    want = []
+    for call, args, out, _ in jobs:
+        assert call(*args) == 0
+        torch.cuda.synchronize()
+        want.append(out.clone())
+        out.zero_()
+    torch.cuda.synchronize()
+    failed, gate = [0] * len(jobs), threading.Barrier(len(jobs))
+
+    def run(k):
+        call, args, *_ = jobs[k]
+        gate.wait()
+        for _ in range(20000):
+            failed[k] += call(*args) != 0
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * len(jobs)
+    for (_, _, out, _), w in zip(jobs, want):
+        assert torch.equal(out, w)
+    assert tsl.tsenor_error_count() == 0
