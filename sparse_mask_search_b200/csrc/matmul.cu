@@ -264,6 +264,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         // 32 of the contracted axis: 32 bytes of a row, or 32 rows
         const uint32_t step_a = (p.a_t ? 4096 : 32) >> 4, step_b = (p.b_t ? 4096 : 32) >> 4;
         tmem_alloc<1>(slot, kTmemCols);
+        prior_done();                            // no limited wait counts the time of the kernel before
         const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(slot), ts = tmem + 2 * kTile;
         int st = 0;
         unsigned phase = 0, n = 0;
@@ -480,6 +481,7 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             for (int i = 0; i < kPairStages && i < issued; ++i)
                 mbar_wait_bounded(full + i, unsigned((issued - 1 - i) / kPairStages) & 1);
     } else if (warp == 1 && rank == 0) {
+        prior_done();                            // no limited wait counts the time of the kernel before
         const uint32_t idesc = mma_desc(kPairTile, kPairTile, p.a_t, p.b_t);
         const uint32_t step_a = (p.a_t ? 4096 : 32) >> 4, step_b = (p.b_t ? 4096 : 32) >> 4;
         int st = 0;

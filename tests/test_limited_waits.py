@@ -1,0 +1,40 @@
+"""The limited waits of the products and the distillation kernels, read from their sources."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_mask_search_b200", "csrc")
+
+
+def _source(name):
+    return re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+
+
+def _kernels(name):
+    """{kernel: body} of a source."""
+    text, found = _source(name), {}
+    for m in re.finditer(r"__global__[^;{]*?(\w+_kernel)\(", text):
+        depth, at = 0, text.index("{", m.end())
+        for i in range(at, len(text)):
+            depth += {"{": 1, "}": -1}.get(text[i], 0)
+            if depth == 0:
+                break
+        found[m.group(1)] = text[at:i + 1]
+    return found
+
+
+@pytest.mark.parametrize("name,count", [("quantize.cu", 2), ("matmul.cu", 2), ("distill.cu", 3)])
+def test_no_limit_counts_the_time_of_the_kernel_before(name, count):
+    # a thread waits for the kernel before without a limit first: in one place for all, or warp 1 in its own branch
+    limited = re.compile(r"\b(\w+_bounded|warp_wait\w*|wait_long)\(")
+    kernels = _kernels(name)
+    assert len(kernels) == count
+    for body in kernels.values():
+        waits = [m.group(1).strip() for m in re.finditer(r"([^;{}]*)\bprior_done\(\);", body)]
+        first = limited.search(body)
+        assert first is None or body.index("prior_done();") < first.start()
+        if waits != [""]:
+            assert waits == ["if (warp != 1)", ""]
+            branch = body[re.search(r"else if \(warp == 1\b", body).start():]
+            assert branch.index("prior_done();") < limited.search(branch).start()
