@@ -482,7 +482,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
         // the columns of a row's entries, once the workers have written the row (its number here: n)
         auto write_targets = [&](int64_t row, unsigned n) {
             const int b = n & 1;
-            if (!mbar_sleep_bounded(done + b, (n >> 1) & 1)) return false;
+            if (!warp_sleep(done + b, (n >> 1) & 1)) return false;
             if (!STEP || row_by[b] == 0.f) return true;
             const float scale = row_scale[b], m = row_high[b], by = row_by[b];
             auto* g = static_cast<typename T::storage*>(a.grad) + row * a.ldg;
@@ -527,7 +527,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
             if (lane == 0) mbar_arrive(told + b);
             if (i > 0 && warp == kWarps) {
                 for (int s = 0; s < segments && !stalled; ++s) {
-                    if (!mbar_sleep_bounded(free + s, (i - 1) & 1)) stalled = true;
+                    if (!warp_sleep(free + s, (i - 1) & 1)) stalled = true;
                     else if (lane == 0) copy(s);
                     __syncwarp();
                 }
@@ -538,7 +538,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
         if (STEP && i > 0 && !stalled && !write_targets(first + (i - 1) * step, i - 1)) stalled = true;
         // copies in flight end before the block does
         if (stalled && warp == kWarps)
-            for (int s = 0; s < segments; ++s) mbar_sleep_bounded(full + s, i & 1);
+            for (int s = 0; s < segments; ++s) warp_sleep(full + s, i & 1);
     } else {
         unsigned i = 0, joins = 0;
         for (int64_t row = first; row < a.rows; row += step, ++i) {
@@ -554,7 +554,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
             // one pass over the slice; a NaN or +inf anywhere makes the sum one too
             Norm norm{-INFINITY, 0.f};
             for (int s = 0; s < segments; ++s) {
-                if (!mbar_sleep_bounded(full + s, i & 1)) { stalled = true; break; }
+                if (!warp_sleep(full + s, i & 1)) { stalled = true; break; }
                 // Written before the first segment began.  A row that is not read waits for its (empty) segments all the
                 // same: its arrivals on free[s] must not overtake the copying warp's wait on them.
                 if (STEP && flags[b]) continue;
@@ -573,7 +573,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
                 }
                 if (!STEP) leave(free + s);
             }
-            if (!mbar_sleep_bounded(told + b, (i >> 1) & 1)) stalled = true;
+            if (!warp_sleep(told + b, (i >> 1) & 1)) stalled = true;
             if (Workers::any(stalled)) { stalled = true; break; }
             const bool empty = flags[b] & 1;
             bool failed = flags[b] & 2;
@@ -603,7 +603,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
                     asm volatile("st.shared::cluster.v2.f64 [%0], {%1, %2};" ::"r"(to), "d"(terms.gap), "d"(terms.mass) : "memory");
                     cluster_arrive(cluster_addr(smem_u32(joined + j), t));
                 }
-                if (!mbar_cluster_sleep_bounded(joined + j, (joins >> 1) & 1)) stalled = true;
+                if (!warp_cluster_sleep(joined + j, (joins >> 1) & 1)) stalled = true;
                 if (Workers::any(stalled)) { stalled = true; break; }
                 ++joins;
                 norm = join(slices, scale2, [&](int k) { return share[j][k].norm; });
@@ -657,6 +657,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
         }
     }
     if (stalled && lane == 0) atomicAdd(&g_row_failures, 1ull);
+    __syncwarp();
     if (slices > 1) cluster_sync();              // no peer writes here any more
 }
 

@@ -46,7 +46,7 @@ constexpr int kPad = 132;                        // floats to a staged row: 16-b
 // An epilogue waits for as long as a tile's sums take: the bound grows with their number.
 __device__ __forceinline__ bool wait_long(uint64_t* bar, unsigned parity, int64_t blocks) {
     for (int64_t i = 0; i <= blocks / 64; ++i)
-        if (mbar_sleep_bounded(bar, parity)) return true;
+        if (warp_sleep(bar, parity)) return true;
     return false;
 }
 
@@ -237,7 +237,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const int64_t tm = t % p.tiles_m, tn = t / p.tiles_m;
             const int m = int(tm * kTile), n = int(tn * kTile);
             for (int64_t kb = k0; kb < k1; ++kb) {
-                if (!mbar_wait_bounded(empty + st, phase ^ 1)) { stalled = true; break; }
+                if (!warp_wait(empty + st, phase ^ 1)) { stalled = true; break; }
                 if (elect_one()) {
                     const bool scales = kb == k0 || kb % 4 == 0;
                     mbar_arrive_expect_tx(full + st, p.a_bytes + kTileBytes + (scales ? 2 * kScaleBytes : 0));
@@ -258,7 +258,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         // copies in flight end before the block does
         if (stalled)
             for (int i = 0; i < p.stages && i < issued; ++i)
-                mbar_wait_bounded(full + i, unsigned((issued - 1 - i) / p.stages) & 1);
+                warp_wait(full + i, unsigned((issued - 1 - i) / p.stages) & 1);
     } else if (warp == 1) {
         const uint32_t idesc = mma_desc(kTile, kTile, p.a_t, p.b_t);
         // 32 of the contracted axis: 32 bytes of a row, or 32 rows
@@ -269,11 +269,11 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         int st = 0;
         unsigned phase = 0, n = 0;
         for (int64_t t = first; t < tiles && !stalled; t += step, ++n) {
-            if (n > 1 && !mbar_wait_bounded(room + (n & 1), ((n >> 1) - 1) & 1)) { stalled = true; break; }
+            if (n > 1 && !warp_wait(room + (n & 1), ((n >> 1) - 1) & 1)) { stalled = true; break; }
             tmem_fence_after();
             const uint32_t d = tmem + (n & 1) * kTile;
             for (int64_t kb = k0; kb < k1; ++kb) {
-                if (!mbar_wait_bounded(full + st, phase)) { stalled = true; break; }
+                if (!warp_wait(full + st, phase)) { stalled = true; break; }
                 tmem_fence_after();
                 if (elect_one()) {
                     if (kb == k0 || kb % 4 == 0) {
@@ -458,7 +458,7 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const int64_t a128 = tm * 2 + rank, b128 = tn * 2 + rank;
             const int m = int(a128 * kTile), n = int(b128 * kTile);
             for (int64_t kb = 0; kb < blocks; ++kb) {
-                if (!mbar_wait_bounded(empty + st, phase ^ 1)) { stalled = true; break; }
+                if (!warp_wait(empty + st, phase ^ 1)) { stalled = true; break; }
                 if (elect_one()) {
                     const uint32_t bar = full0 + st * 8;
                     if (rank == 0) mbar_arrive_expect_tx(full + st, 4 * kTileBytes + (kb % 4 == 0 ? 6 * kScaleBytes : 0));
@@ -479,7 +479,7 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         // copies in flight end before the pair does (rank 0's barriers count both CTAs' bytes)
         if (stalled && rank == 0)
             for (int i = 0; i < kPairStages && i < issued; ++i)
-                mbar_wait_bounded(full + i, unsigned((issued - 1 - i) / kPairStages) & 1);
+                warp_wait(full + i, unsigned((issued - 1 - i) / kPairStages) & 1);
     } else if (warp == 1 && rank == 0) {
         prior_done();                            // no limited wait counts the time of the kernel before
         const uint32_t idesc = mma_desc(kPairTile, kPairTile, p.a_t, p.b_t);
@@ -487,11 +487,11 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         int st = 0;
         unsigned phase = 0, n = 0;
         for (int64_t t = first; t < tiles && !stalled; t += step, ++n) {
-            if (n > 0 && !mbar_wait_bounded(room, (n - 1) & 1)) { stalled = true; break; }
+            if (n > 0 && !warp_wait(room, (n - 1) & 1)) { stalled = true; break; }
             tmem_fence_after();
             const uint32_t d = tmem + (n & 1 ? kSecond : 0);
             for (int64_t kb = 0; kb < blocks; ++kb) {
-                if (!mbar_wait_bounded(full + st, phase)) { stalled = true; break; }
+                if (!warp_wait(full + st, phase)) { stalled = true; break; }
                 tmem_fence_after();
                 if (elect_one()) {
                     if (kb % 4 == 0) {

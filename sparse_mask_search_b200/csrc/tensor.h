@@ -128,33 +128,35 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
         ::"r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
 }
 
-// Polls as mbar_wait_bounded does, each poll asleep for up to 2 us: for warps that have nothing
-// else to do while others work.
-__device__ __forceinline__ bool mbar_sleep_bounded(uint64_t* bar, unsigned parity) {
-    for (unsigned k = 0; k < kTmaPolls; ++k) {
-        uint32_t done;
+// ---- limited waits --------------------------------------------------------------------
+
+// For a converged warp.  The limit is on polls, which lanes make by themselves: if the polls of some ran out and of
+// others did not, the warp would come apart in front of instructions that it has to meet as one, so all lanes
+// get one verdict.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+// The same with each poll asleep for up to 2 us: for warps that have nothing else to do while others work.
+__device__ __forceinline__ bool warp_sleep(uint64_t* bar, unsigned parity) {
+    uint32_t done = 0;
+    for (unsigned k = 0; k < kTmaPolls && !done; ++k)
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done) : "r"(smem_u32(bar)), "r"(parity), "r"(2000u) : "memory");
-        if (done) return true;
-    }
-    return false;
+    return __all_sync(0xffffffffu, done);
 }
-
-// The same for a barrier on which other CTAs of the cluster arrive: what they wrote before is visible after it.
-__device__ __forceinline__ bool mbar_cluster_sleep_bounded(uint64_t* bar, unsigned parity) {
-    for (unsigned k = 0; k < kTmaPolls; ++k) {
-        uint32_t done;
+// And for a barrier on which other CTAs of the cluster arrive: what they wrote before is visible after it.
+__device__ __forceinline__ bool warp_cluster_sleep(uint64_t* bar, unsigned parity) {
+    uint32_t done = 0;
+    for (unsigned k = 0; k < kTmaPolls && !done; ++k)
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done) : "r"(smem_u32(bar)), "r"(parity), "r"(2000u) : "memory");
-        if (done) return true;
-    }
-    return false;
+    return __all_sync(0xffffffffu, done);
 }
 
 // ---- copies and clusters ----------------------------------------------------------------

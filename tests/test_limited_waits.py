@@ -38,3 +38,23 @@ def test_no_limit_counts_the_time_of_the_kernel_before(name, count):
             assert waits == ["if (warp != 1)", ""]
             branch = body[re.search(r"else if \(warp == 1\b", body).start():]
             assert branch.index("prior_done();") < limited.search(branch).start()
+
+
+def test_a_warp_has_one_verdict():
+    # lanes that went on after a wait that other lanes gave up would meet aligned instructions without them
+    for name in ("matmul.cu", "distill.cu"):
+        assert not re.search(r"\bmbar_\w*(bounded|wait|sleep)\b", _source(name))
+    text = _source("tensor.h")
+    polls = [m.start() for m in re.finditer(r"mbarrier\.try_wait|mbar_wait_bounded\(", text)]
+    functions = [m.start() for m in re.finditer(r"\bbool warp_\w+\(", text)]
+    assert len(polls) == len(functions) == 3
+    for start, poll in zip(functions, polls):
+        assert start < poll and re.search(r"return __all_sync\(0xffffffffu, [^;]*;\s*}", text[start:text.index("\n}", start) + 2])
+
+
+@pytest.mark.parametrize("name", ["matmul.cu", "distill.cu"])
+def test_giving_up_is_counted(name):
+    # by lane 0, for its warp
+    for kernel, body in _kernels(name).items():
+        if re.search(r"\bwarp_(wait|sleep|cluster_sleep)\(|\bwait_long\(", body):
+            assert re.search(r"if \(stalled && lane == 0\) atomicAdd\(&g_\w+, 1ull\);\s*__syncwarp\(\);", body), kernel
