@@ -57,8 +57,10 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, int cols) {       // th
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 32 lanes (the warp's quarter of the 128) x 32 columns, one row to a thread.
+// 32 lanes (the warp's quarter of the 128) x 32 columns, one row to a thread.  Both of these are for the warp as one:
+// lanes that stored by themselves meet again first.
 __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&v)[32]) {
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -71,6 +73,7 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&v)[32]) {
 }
 // Waits for all of the warp's loads; v: the registers that are read next, so that no use moves before the wait.
 __device__ __forceinline__ void tmem_wait_load(uint32_t (&v)[32]) {
+    __syncwarp();
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
                    "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),

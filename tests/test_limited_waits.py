@@ -1,4 +1,4 @@
-"""The limited waits of the products and the distillation kernels, read from their sources."""
+"""The limited waits of the products and the distillation kernels, and where lanes of a warp meet, read from their sources."""
 import os
 import re
 
@@ -58,3 +58,13 @@ def test_giving_up_is_counted(name):
     for kernel, body in _kernels(name).items():
         if re.search(r"\bwarp_(wait|sleep|cluster_sleep)\(|\bwait_long\(", body):
             assert re.search(r"if \(stalled && lane == 0\) atomicAdd\(&g_\w+, 1ull\);\s*__syncwarp\(\);", body), kernel
+
+
+def test_lanes_meet_before_tensor_memory_is_read():
+    # the stores between two reads go by lane, some of which may have none
+    text = _source("tensor.h")
+    reads = [m.start() for m in re.finditer(r"tcgen05\.(ld|wait::ld)", text)]
+    assert len(reads) == 2
+    for at in reads:
+        start = text.rindex("__device__", 0, at)
+        assert re.search(r"{\s*__syncwarp\(\);\s*asm volatile\($", text[start:text.rindex("asm volatile(", 0, at) + 13])
