@@ -957,14 +957,8 @@ bool grad_ok(int dtype, const DistillArgs& a) {
 
 }  // namespace
 
-cudaError_t read_row_failures(cudaStream_t st, unsigned long long* count) {
-    unsigned long long v = 0;
-    const unsigned long long zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_row_failures, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_row_failures, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess) *count += v;
-    return e;
+cudaError_t row_failures(unsigned long long** counter) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(counter), g_row_failures);
 }
 
 }  // namespace tsenor

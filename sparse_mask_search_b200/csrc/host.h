@@ -68,10 +68,9 @@ cudaError_t clusters_that_fit(int* count, void (*kernel)(P...), int block, size_
     return cudaOccupancyMaxActiveClusters(count, kernel, &cfg);
 }
 
-// Adds the rows that failed in the distillation kernels on the current device
-// since the last call to *count and resets them (ordered on `st`).
-cudaError_t read_row_failures(cudaStream_t st, unsigned long long* count);
-// The same for the threads of tsenor_matmul's kernels whose bounded wait ran out.
-cudaError_t read_stalled(cudaStream_t st, unsigned long long* count);
+// Counters on the current device that tsenor_error_count adds up and resets: rows that failed in the distillation kernels,
+// and warps of tsenor_matmul's kernels whose limited wait ran out.
+cudaError_t row_failures(unsigned long long** counter);
+cudaError_t stalls(unsigned long long** counter);
 
 }  // namespace tsenor

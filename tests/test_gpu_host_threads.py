@@ -89,3 +89,37 @@ def test_calls_of_different_sizes_from_several_threads(make, sizes):
     for (_, _, out, _), w in zip(jobs, want):
         assert torch.equal(out, w)
     assert tsl.tsenor_error_count() == 0
+
+
+def test_failures_counted_on_one_stream_while_another_reads_the_count():
+    # every failure is in one number, none is lost between a read and the reset
+    rows, calls = 64, 1500
+    z = torch.full((rows, 8), torch.nan, device="cuda")
+    index, top = torch.zeros((rows, 1), dtype=torch.int32, device="cuda"), torch.zeros((rows, 1), device="cuda")
+    W = torch.full((64, 64), torch.nan, device="cuda")
+    tsl.tsenor_error_count()
+    torch.cuda.synchronize()
+    seen, stop, errors = [], threading.Event(), []
+
+    def read():
+        try:
+            stream = torch.cuda.Stream()
+            while not stop.is_set():
+                seen.append(tsl.tsenor_error_count(stream))
+        except Exception as e:                          # reported below, in the main thread
+            errors.append(e)
+
+    readers = [threading.Thread(target=read) for _ in range(2)]
+    for t in readers:
+        t.start()
+    for _ in range(calls):
+        tsl.tsenor_distill_loss(z, index, top)
+    for _ in range(10):
+        tsl.tsenor_mask(W, 16, 32, 20.0, 5, 1)
+    torch.cuda.synchronize()
+    stop.set()
+    for t in readers:
+        t.join()
+    assert not errors, errors
+    assert sum(seen) + tsl.tsenor_error_count() == rows * calls + 4 * 10
+    assert tsl.tsenor_error_count() == 0
