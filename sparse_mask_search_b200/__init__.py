@@ -376,7 +376,8 @@ def _on(device, stream):
     """The device and the stream of a call: what it allocates belongs to that stream."""
     import torch
     if stream is not None and not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        handle = int(stream)                    # ExternalStream takes 0 for a new stream of its own
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     with torch.cuda.device(device), torch.cuda.stream(stream):
         yield
 

@@ -1,4 +1,4 @@
-"""Several host threads in the 8-bit and distillation calls."""
+"""Host threads and streams of the 8-bit and distillation calls."""
 import threading
 
 import pytest
@@ -123,3 +123,20 @@ def test_failures_counted_on_one_stream_while_another_reads_the_count():
     assert not errors, errors
     assert sum(seen) + tsl.tsenor_error_count() == rows * calls + 4 * 10
     assert tsl.tsenor_error_count() == 0
+
+
+def test_stream_zero_is_the_default_stream():
+    device = torch.device("cuda", torch.cuda.current_device())
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with tsl._on(device, 0):
+            assert torch.cuda.current_stream().cuda_stream == torch.cuda.default_stream().cuda_stream == 0
+    x = torch.randn((300, 500), device="cuda")
+    want = tsl.tsenor_quantize(x)
+    out = tsl.QuantizedMatrix(torch.empty_strided((300, 500), (512, 1), dtype=torch.float8_e4m3fn, device="cuda"),
+                              torch.zeros_like(want.scales))
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                       # the default stream is busy: the call waits its turn there
+    x.neg_()
+    tsl.tsenor_quantize(x, out=out, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out.values.float(), -want.values.float()) and torch.equal(out.scales, want.scales)
