@@ -378,6 +378,8 @@ def _on(device, stream):
     if stream is not None and not hasattr(stream, "cuda_stream"):
         handle = int(stream)                    # ExternalStream takes 0 for a new stream of its own
         stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    elif getattr(stream, "device", device) != device:
+        raise ValueError(f"stream must be on {device}, is on {stream.device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
         yield
 
