@@ -189,10 +189,10 @@ struct TileSmem {
         turn = s + stages * 2 * kScaleBytes;
         bars = turn + 4 * 32 * 33 * 4;
     }
-    __host__ __device__ unsigned bytes(int stages) const { return bars + (2 * stages + 4) * 8 + 16; }
+    __host__ __device__ unsigned bytes(int stages) const { return bars + (2 * stages + 5) * 8 + 16; }
 };
 // The most that a launch asks for: the smallest stage (8 rows of A) gives 12 stages at most.
-constexpr unsigned kTileMost = kStageBytes + (2 * (kStageBytes / (9 * 1024 * 2)) + 4) * 8 + 16 + 1024;
+constexpr unsigned kTileMost = kStageBytes + (2 * (kStageBytes / (9 * 1024 * 2)) + 5) * 8 + 16 + 1024;
 static_assert(kTileMost <= 227 * 1024, "shared memory of a CTA");
 
 template <bool SPLIT, bool BF16OUT>
@@ -206,7 +206,8 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     uint64_t* empty = full + p.stages;
     uint64_t* ready = empty + p.stages;          // an accumulator is complete
     uint64_t* room = ready + 2;                  // an accumulator has been read
-    uint32_t* slot = reinterpret_cast<uint32_t*>(room + 2);
+    uint64_t* over = room + 2;                   // no product is in flight any more
+    uint32_t* slot = reinterpret_cast<uint32_t*>(over + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = SPLIT ? cluster_rank() : 0;
     const int64_t tiles = p.tiles_m * p.tiles_n, blocks = (p.k + kTile - 1) / kTile;
@@ -222,6 +223,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             mbar_init(ready + i, 1);
             mbar_init(room + i, 4);
         }
+        mbar_init(over, 1);
         mbar_init_fence();
     }
     let_next_start();
@@ -232,7 +234,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     if (warp == 0) {                             // loads start while warp 1 gets its tensor memory
         int st = 0;
         unsigned phase = 0;
-        int64_t issued = 0;
+        bool around = false;                     // every stage has been used
         for (int64_t t = first; t < tiles && !stalled; t += step) {
             const int64_t tm = t % p.tiles_m, tn = t / p.tiles_m;
             const int m = int(tm * kTile), n = int(tn * kTile);
@@ -251,14 +253,12 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     }
                 }
                 __syncwarp();
-                ++issued;
-                if (++st == p.stages) { st = 0; phase ^= 1; }
+                if (++st == p.stages) { st = 0; phase ^= 1; around = true; }
             }
         }
-        // copies in flight end before the block does
-        if (stalled)
-            for (int i = 0; i < p.stages && i < issued; ++i)
-                warp_wait(full + i, unsigned((issued - 1 - i) / p.stages) & 1);
+        // copies in flight end before the block does, whichever warp gave up
+        for (int i = 0; i < p.stages; ++i)
+            if ((around || i < st) && !warp_drain(full + i, i < st ? phase : phase ^ 1)) stalled = true;
     } else if (warp == 1) {
         const uint32_t idesc = mma_desc(kTile, kTile, p.a_t, p.b_t);
         // 32 of the contracted axis: 32 bytes of a row, or 32 rows
@@ -295,6 +295,10 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             if (!stalled && elect_one()) mma_commit(ready + (n & 1));
             __syncwarp();
         }
+        // products in flight end before their tiles and tensor memory go, whichever warp gave up
+        if (elect_one()) mma_commit(over);
+        __syncwarp();
+        if (!warp_drain(over, 0)) stalled = true;
     } else {
         const int quarter = warp & 3;            // the lanes of tensor memory that a warp may read
         float* turn = reinterpret_cast<float*>(smem + at.turn) + quarter * 32 * 33;
@@ -395,7 +399,7 @@ constexpr int kGroupM = 16;                      // tiles of 256 rows walked tog
 
 struct PairSmem {
     static constexpr unsigned a = 0, b = kPairStages * kTileBytes, s = 2 * b, staged = s + kPairStages * 3 * kScaleBytes,
-                              bars = staged + 8 * 32 * 33 * 4, bytes = bars + (2 * kPairStages + 3) * 8 + 16;
+                              bars = staged + 8 * 32 * 33 * 4, bytes = bars + (2 * kPairStages + 4) * 8 + 2 * 8 + 2 * 4;
 };
 
 // Tile t of the walk: groups of kGroupM tile rows, column by column within a group.
@@ -417,7 +421,10 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     uint64_t* empty = full + kPairStages;
     uint64_t* ready = empty + kPairStages;       // an accumulator is complete (one barrier for each of the two)
     uint64_t* room = ready + 2;                  // the next accumulator may be written
-    uint32_t* slot = reinterpret_cast<uint32_t*>(room + 1);
+    uint64_t* over = room + 1;                   // no product is in flight any more
+    int64_t* issued = reinterpret_cast<int64_t*>(over + 1);      // stages that each CTA's copies went to; in rank 0
+    uint32_t* slot = reinterpret_cast<uint32_t*>(issued + 2);
+    uint32_t* gave_up = slot + 1;                // some warp of the pair
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned rank = cluster_rank();
     const int64_t tiles_m = (p.m + kPairTile - 1) / kPairTile, tiles_n = (p.n + kPairTile - 1) / kPairTile;
@@ -432,6 +439,8 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         mbar_init(ready, 1);
         mbar_init(ready + 1, 1);
         mbar_init(room, 16);                     // the epilogue warps of both CTAs; used in rank 0
+        mbar_init(over, 1);
+        *gave_up = 0;
         mbar_init_fence();
     }
     if (warp == 2) tmem_alloc<2>(slot, 512);
@@ -451,7 +460,7 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         const uint32_t full0 = cluster_addr(smem_u32(full), 0);
         int st = 0;
         unsigned phase = 0;
-        int64_t issued = 0;
+        int64_t count = 0;
         for (int64_t t = first; t < tiles && !stalled; t += step) {
             int64_t tm, tn;
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
@@ -472,14 +481,11 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     }
                 }
                 __syncwarp();
-                ++issued;
+                ++count;
                 if (++st == kPairStages) { st = 0; phase ^= 1; }
             }
         }
-        // copies in flight end before the pair does (rank 0's barriers count both CTAs' bytes)
-        if (stalled && rank == 0)
-            for (int i = 0; i < kPairStages && i < issued; ++i)
-                warp_wait(full + i, unsigned((issued - 1 - i) / kPairStages) & 1);
+        if (lane == 0) cluster_store(cluster_addr(smem_u32(issued + rank), 0), count);
     } else if (warp == 1 && rank == 0) {
         prior_done();                            // no limited wait counts the time of the kernel before
         const uint32_t idesc = mma_desc(kPairTile, kPairTile, p.a_t, p.b_t);
@@ -514,6 +520,10 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             if (!stalled && elect_one()) mma_commit_pair(ready + (n & 1));
             __syncwarp();
         }
+        // products in flight end before their tiles and tensor memory go, whichever warp gave up
+        if (elect_one()) mma_commit_pair(over);
+        __syncwarp();
+        if (!warp_drain(over, 0)) stalled = true;
     } else if (warp >= 4) {
         // two warps to a quarter of the lanes, 128 columns each
         const int quarter = warp & 3, half = (warp - 4) >> 2;
@@ -559,11 +569,32 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             }
         }
     }
+    if (stalled && lane < 2) cluster_store(cluster_addr(smem_u32(gave_up), lane), 1u);
     if (stalled && lane == 0) atomicAdd(&g_stalled, 1ull);
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
     cluster_sync();                              // both CTAs are done with each other's barriers and tensor memory
+    if (warp == 1 && rank == 1) warp_drain(over, 0);         // the products' arrivals on this CTA's barriers
+    if (*gave_up) {                              // as a rule every copy has been multiplied
+        // Copies in flight end before the pair does.  A stage counts the bytes of both CTAs, of which one may have
+        // issued fewer: those bytes are not expected, or, where rank 0 did already, counted as if they had come.
+        if (warp == 0 && rank == 0) {
+            const int64_t least = issued[0] < issued[1] ? issued[0] : issued[1], most = issued[0] + issued[1] - least;
+            for (int64_t i = least; i < most; ++i) {         // kPairStages at most
+                const unsigned bytes = 2 * kTileBytes + (i % blocks % 4 == 0 ? 3 * kScaleBytes : 0);
+                if (lane == 0) {
+                    if (issued[0] < issued[1]) mbar_arrive_expect_tx(full + i % kPairStages, bytes);
+                    else mbar_complete_tx(full + i % kPairStages, bytes);
+                }
+            }
+            __syncwarp();
+            for (int64_t i = most < kPairStages ? 0 : most - kPairStages; i < most; ++i)
+                warp_drain(full + i % kPairStages, unsigned(i / kPairStages) & 1);
+        }
+        __syncwarp();
+        cluster_sync();
+    }
     if (warp == 2) tmem_free<2>(tmem, 512);
 }
 
@@ -672,6 +703,10 @@ cudaError_t launch(const MatmulArgs& p, const uint8_t* a, int64_t lda, const uin
 }
 
 }  // namespace
+
+#ifdef TSENOR_GIVE_UP
+extern "C" int give_up_products(unsigned polls, unsigned one_in) { return give_up(polls, one_in); }
+#endif
 
 cudaError_t stalls(unsigned long long** counter) {
     return cudaGetSymbolAddress(reinterpret_cast<void**>(counter), g_stalled);

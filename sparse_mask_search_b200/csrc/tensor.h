@@ -133,16 +133,37 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 
 // ---- limited waits --------------------------------------------------------------------
 
+// Polls of a wait.  In a build for tests they are drawn: none for one wait of g_give_up_one_in, g_wait_polls for the others.
+#ifdef TSENOR_GIVE_UP
+static __device__ unsigned g_wait_polls = kTmaPolls, g_give_up_one_in;
+inline int give_up(unsigned polls, unsigned one_in) {
+    const cudaError_t e = cudaMemcpyToSymbol(g_wait_polls, &polls, sizeof(polls));
+    return e != cudaSuccess ? int(e) : int(cudaMemcpyToSymbol(g_give_up_one_in, &one_in, sizeof(one_in)));
+}
+__device__ __forceinline__ unsigned wait_polls() {
+    const unsigned in = *static_cast<volatile unsigned*>(&g_give_up_one_in);
+    const unsigned mixed = (unsigned(clock64()) ^ (blockIdx.x * 64u + threadIdx.x / 32u) * 0x9e3779b9u) * 2654435761u;
+    return in && (mixed >> 8) % in == 0 ? 0u : *static_cast<volatile unsigned*>(&g_wait_polls);
+}
+#else
+__device__ __forceinline__ unsigned wait_polls() { return kTmaPolls; }
+#endif
+
 // For a converged warp.  The limit is on polls, which lanes make by themselves: if the polls of some ran out and of
 // others did not, the warp would come apart in front of instructions that it has to meet as one, so all lanes
 // get one verdict.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned polls = wait_polls()) {
+    bool done = false;
+    for (unsigned k = 0; k < polls && !done; ++k) done = mbar_try_wait(bar, parity);
+    return __all_sync(0xffffffffu, done);
 }
-// The same with each poll asleep for up to 2 us: for warps that have nothing else to do while others work.
+// For what a kernel has in flight when it ends, after a wait that gave up too.
+__device__ __forceinline__ bool warp_drain(uint64_t* bar, unsigned parity) { return warp_wait(bar, parity, kTmaPolls); }
+// As warp_wait, with each poll asleep for up to 2 us: for warps that have nothing else to do while others work.
 __device__ __forceinline__ bool warp_sleep(uint64_t* bar, unsigned parity) {
+    const unsigned polls = wait_polls();
     uint32_t done = 0;
-    for (unsigned k = 0; k < kTmaPolls && !done; ++k)
+    for (unsigned k = 0; k < polls && !done; ++k)
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
@@ -152,8 +173,9 @@ __device__ __forceinline__ bool warp_sleep(uint64_t* bar, unsigned parity) {
 }
 // And for a barrier on which other CTAs of the cluster arrive: what they wrote before is visible after it.
 __device__ __forceinline__ bool warp_cluster_sleep(uint64_t* bar, unsigned parity) {
+    const unsigned polls = wait_polls();
     uint32_t done = 0;
-    for (unsigned k = 0; k < kTmaPolls && !done; ++k)
+    for (unsigned k = 0; k < polls && !done; ++k)
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
@@ -185,6 +207,18 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // Arrival on a barrier of any CTA of the cluster.
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Counts `bytes` on `bar` as if a copy had brought them.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, unsigned bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+// Stores to an address of a CTA of the cluster.
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t x) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ void cluster_store(uint32_t addr, int64_t x) {
+    asm volatile("st.shared::cluster.s64 [%0], %1;" ::"r"(addr), "l"(x) : "memory");
 }
 
 // 32 bytes to a 32-byte aligned address in one store.

@@ -1,10 +1,18 @@
 """The limited waits of the products and the distillation kernels on the GPU."""
+import ctypes as C
+import os
+import subprocess
+
 import pytest
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import sparse_mask_search_b200 as tsl  # noqa: E402
+from sparse_mask_search_b200 import build  # noqa: E402
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+SOURCES = ["matmul.cu"]
 
 
 def _ones(rows, cols):
@@ -23,4 +31,69 @@ def test_product_behind_a_long_one_on_few_sms(m):
     tsl.tsenor_matmul(long, long, dtype=torch.float32)
     got = tsl.tsenor_matmul(a, b)
     assert torch.equal(got, want)
+    assert tsl.tsenor_error_count() == 0
+
+
+# ---- waits that run out ---------------------------------------------------------------------------
+#
+# A build of the same sources in which a wait gives up as if its polls had run out: at random, one in so many.  Each
+# kernel has to end by itself with its copies and products done, count that it gave up, and leave the GPU as it
+# was: the calls right behind it are right.
+
+NEVER = (1 << 18, 0)                                     # the library's own limit, and no wait that gives up
+
+
+@pytest.fixture(scope="module")
+def giving_up():
+    lib = os.path.join(HERE, "_build", "libgive_up.so")
+    sources = [os.path.join(build.HERE, "csrc", f) for f in SOURCES] + [os.path.join(HERE, "give_up.cu")]
+    deps = build.sources() + [os.path.join(HERE, "give_up.cu")]
+    if not os.path.exists(lib) or os.path.getmtime(lib) < max(os.path.getmtime(s) for s in deps):
+        os.makedirs(os.path.dirname(lib), exist_ok=True)
+        subprocess.run([build.nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "--threads", "0",
+                        "-Xcompiler", "-fPIC", "-shared", "-DTSENOR_GIVE_UP", *sources, "-o", lib], check=True)
+    L = C.CDLL(lib)
+    ours = tsl.lib()
+    L.tsenor_matmul.argtypes = ours.tsenor_matmul.argtypes
+    L.give_up_products.argtypes = [C.c_uint, C.c_uint]
+    L.give_up_count.restype = C.c_longlong
+    return L
+
+
+# shares of a tile; one tile to a block; tiles that blocks walk, to rows off 32 bytes too; pairs with one tile, with several, to rows off 32 bytes
+PRODUCTS = [("nt", 60, 256, 4096, 256), ("nt", 1, 11008, 4096, 11008), ("nn", 300, 9000, 1100, 9000), ("tn", 1500, 1300, 777, 1301),
+            ("tn", 2048, 2900, 1100, 2901), ("nn", 512, 8000, 4096, 8000), ("nt", 2048, 4096, 2048, 4096), ("tn", 2300, 4100, 3300, 4101)]
+
+
+@pytest.mark.parametrize("form,m,n,k,ldo", PRODUCTS)
+@pytest.mark.parametrize("one_in", [1, 3, 20, 200, 3000])
+def test_products_that_give_up(giving_up, form, m, n, k, ldo, one_in):
+    sa, sb = {"nt": ((m, k), (n, k)), "nn": ((m, k), (k, n)), "tn": ((k, m), (k, n))}[form]
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    a = tsl.tsenor_quantize(torch.randn(sa, generator=g, device="cuda"), "tile")
+    b = tsl.tsenor_quantize(torch.randn(sb, generator=g, device="cuda"), "tile")
+    out = torch.zeros((m, ldo), dtype=torch.bfloat16, device="cuda")
+    on_a, on_b = (a.scales_t if form == "tn" else a.scales), (b.scales if form == "nt" else b.scales_t)
+    args = (tsl.FORMS[form], a.values.data_ptr(), a.values.stride(0), on_a.data_ptr(), b.values.data_ptr(), b.values.stride(0),
+            on_b.data_ptr(), m, n, k, None, out.data_ptr(), tsl.TSENOR_BF16, ldo, torch.cuda.current_stream().cuda_stream)
+    want = tsl.tsenor_matmul(a, b, form)
+    assert giving_up.give_up_products(200, one_in) == 0 and giving_up.give_up_count() == 0
+    gave_up = 0
+    for _ in range(12):
+        out.zero_()
+        assert giving_up.tsenor_matmul(*args) == 0
+        behind = tsl.tsenor_matmul(a, b, form)
+        count = giving_up.give_up_count()
+        assert count >= 0 and torch.equal(behind, want)
+        if count == 0:
+            assert torch.equal(out[:, :n], want)
+        gave_up += count
+    assert gave_up > 0 or one_in > 200
+    for _ in range(12):                                  # without a pause in between
+        assert giving_up.tsenor_matmul(*args) == 0
+    behind = tsl.tsenor_matmul(a, b, form)
+    assert giving_up.give_up_count() >= 0 and torch.equal(behind, want)
+    assert giving_up.give_up_products(*NEVER) == 0
+    assert giving_up.tsenor_matmul(*args) == 0
+    assert giving_up.give_up_count() == 0 and torch.equal(out[:, :n], want)
     assert tsl.tsenor_error_count() == 0

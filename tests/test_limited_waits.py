@@ -45,11 +45,13 @@ def test_a_warp_has_one_verdict():
     for name in ("matmul.cu", "distill.cu"):
         assert not re.search(r"\bmbar_\w*(bounded|wait|sleep)\b", _source(name))
     text = _source("tensor.h")
-    polls = [m.start() for m in re.finditer(r"mbarrier\.try_wait|mbar_wait_bounded\(", text)]
+    assert len(re.findall(r"\bmbar_try_wait\(|mbarrier\.try_wait", text)) == 3
     functions = [m.start() for m in re.finditer(r"\bbool warp_\w+\(", text)]
-    assert len(polls) == len(functions) == 3
-    for start, poll in zip(functions, polls):
-        assert start < poll and re.search(r"return __all_sync\(0xffffffffu, [^;]*;\s*}", text[start:text.index("\n}", start) + 2])
+    assert len(functions) == 4
+    for start in functions:
+        body = text[text.index("{", start):]
+        body = body[:re.search(r";\s*}\s", body).end()]
+        assert re.search(r"return (__all_sync\(0xffffffffu, done\)|warp_wait\([^;]*\));\s*}\s$", body), body
 
 
 @pytest.mark.parametrize("name", ["matmul.cu", "distill.cu"])
