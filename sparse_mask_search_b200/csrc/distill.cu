@@ -478,7 +478,8 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
     bool stalled = false;
 
     if (warp >= kWarps) {
-        unsigned i = 0;
+        unsigned i = 0, newest = 0;              // the row (its number here) of the newest copies,
+        int copied = 0;                          // and how many of its segments they bring; in the warp that copies
         // the columns of a row's entries, once the workers have written the row (its number here: n)
         auto write_targets = [&](int64_t row, unsigned n) {
             const int b = n & 1;
@@ -511,6 +512,7 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
             };
             if (i == 0 && t == kThreads)
                 for (int s = 0; s < segments; ++s) copy(s);
+            if (i == 0) copied = segments;
             const int e = t - kThreads;
             if (e < slice.extras()) extra[b][e] = read<T>(z + slice.extra(e));
             if (!empty && !(STEP && bad)) {
@@ -526,9 +528,10 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
             __syncwarp();
             if (lane == 0) mbar_arrive(told + b);
             if (i > 0 && warp == kWarps) {
-                for (int s = 0; s < segments && !stalled; ++s) {
-                    if (!warp_sleep(free + s, (i - 1) & 1)) stalled = true;
-                    else if (lane == 0) copy(s);
+                newest = i;
+                for (copied = 0; copied < segments; ++copied) {
+                    if (!warp_sleep(free + copied, (i - 1) & 1)) { stalled = true; break; }
+                    if (lane == 0) copy(copied);
                     __syncwarp();
                 }
             }
@@ -536,9 +539,10 @@ loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const i
             if (Extra::any(stalled)) { stalled = true; break; }
         }
         if (STEP && i > 0 && !stalled && !write_targets(first + (i - 1) * step, i - 1)) stalled = true;
-        // copies in flight end before the block does
-        if (stalled && warp == kWarps)
-            for (int s = 0; s < segments; ++s) warp_sleep(full + s, i & 1);
+        // copies in flight end before the block does, whichever warp gave up
+        if (warp == kWarps)
+            for (int s = 0; s < segments; ++s)
+                if ((s < copied || newest > 0) && !warp_drain(full + s, (s < copied ? newest : newest - 1) & 1)) stalled = true;
     } else {
         unsigned i = 0, joins = 0;
         for (int64_t row = first; row < a.rows; row += step, ++i) {
@@ -956,6 +960,10 @@ bool grad_ok(int dtype, const DistillArgs& a) {
 }
 
 }  // namespace
+
+#ifdef TSENOR_GIVE_UP
+extern "C" int give_up_distillation(unsigned polls, unsigned one_in) { return give_up(polls, one_in); }
+#endif
 
 cudaError_t row_failures(unsigned long long** counter) {
     return cudaGetSymbolAddress(reinterpret_cast<void**>(counter), g_row_failures);

@@ -12,7 +12,7 @@ import sparse_mask_search_b200 as tsl  # noqa: E402
 from sparse_mask_search_b200 import build  # noqa: E402
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-SOURCES = ["matmul.cu"]
+SOURCES = ["matmul.cu", "distill.cu"]
 
 
 def _ones(rows, cols):
@@ -54,8 +54,9 @@ def giving_up():
                         "-Xcompiler", "-fPIC", "-shared", "-DTSENOR_GIVE_UP", *sources, "-o", lib], check=True)
     L = C.CDLL(lib)
     ours = tsl.lib()
-    L.tsenor_matmul.argtypes = ours.tsenor_matmul.argtypes
-    L.give_up_products.argtypes = [C.c_uint, C.c_uint]
+    for name in ("tsenor_matmul", "tsenor_distill_loss", "tsenor_distill_step"):
+        getattr(L, name).argtypes = getattr(ours, name).argtypes
+    L.give_up_products.argtypes = L.give_up_distillation.argtypes = [C.c_uint, C.c_uint]
     L.give_up_count.restype = C.c_longlong
     return L
 
@@ -96,4 +97,50 @@ def test_products_that_give_up(giving_up, form, m, n, k, ldo, one_in):
     assert giving_up.give_up_products(*NEVER) == 0
     assert giving_up.tsenor_matmul(*args) == 0
     assert giving_up.give_up_count() == 0 and torch.equal(out[:, :n], want)
+    assert tsl.tsenor_error_count() == 0
+
+
+# slices of a cluster, one row to it and several; rows of one CTA, one and several; fp32 rows of several segments
+@pytest.mark.parametrize("dtype,rows,vocab", [("bf16", 3, 32000), ("bf16", 400, 131072), ("f32", 100, 40000), ("f32", 147, 3001),
+                                              ("f32", 90, 262143), ("bf16", 1, 900)])
+@pytest.mark.parametrize("step", [False, True])
+@pytest.mark.parametrize("one_in", [1, 3, 20, 200, 3000])
+def test_distillation_that_gives_up(giving_up, dtype, rows, vocab, step, one_in):
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    z = torch.randn((rows, vocab), generator=g, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    value, index = z.float().topk(7, 1)
+    index, value = index.to(torch.int32), value.contiguous()
+    index[::5] = -1
+    loss, lse, grad = torch.zeros((rows,), device="cuda"), torch.zeros((rows,), device="cuda"), torch.zeros_like(z)
+    shared = (z.data_ptr(), int(dtype == "bf16"), rows, vocab, vocab, index.data_ptr(), value.data_ptr(), 7, None, 2.0)
+    stream = torch.cuda.current_stream().cuda_stream
+    if step:
+        outs, ours = (loss, grad), lambda: tsl.tsenor_distill_step(z, index, value, 2.0)
+        call = lambda: giving_up.tsenor_distill_step(*shared, None, loss.data_ptr(), grad.data_ptr(), vocab, stream)
+    else:
+        outs, ours = (loss, lse), lambda: tsl.tsenor_distill_loss(z, index, value, 2.0)
+        call = lambda: giving_up.tsenor_distill_loss(*shared, loss.data_ptr(), lse.data_ptr(), stream)
+    want = ours()
+    same = lambda got: all(torch.equal(x, y) for x, y in zip(got, want))
+    assert giving_up.give_up_distillation(200, one_in) == 0 and giving_up.give_up_count() == 0
+    gave_up = 0
+    for _ in range(8):
+        for t in outs:
+            t.zero_()
+        assert call() == 0
+        behind = ours()
+        count = giving_up.give_up_count()
+        assert count >= 0 and same(behind)
+        if count == 0:
+            assert same(outs)
+        gave_up += count
+    # (the loss of many rows and the step of short ones stream them and wait for nothing)
+    assert gave_up > 0 or one_in > 3 or not step and rows >= 148
+    for _ in range(8):                                   # without a pause in between
+        assert call() == 0
+    behind = ours()
+    assert giving_up.give_up_count() >= 0 and same(behind)
+    assert giving_up.give_up_distillation(*NEVER) == 0
+    assert call() == 0
+    assert giving_up.give_up_count() == 0 and same(outs)
     assert tsl.tsenor_error_count() == 0
