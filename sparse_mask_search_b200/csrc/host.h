@@ -16,11 +16,13 @@ tsenor_status cuda_fail(cudaError_t e, const char* what);
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // encode(), a call of the driver's tensor map encoder: it wants a context, which a host thread has only once it has called the
-// runtime, so that the first call of a thread may have to make it and try again.
+// runtime, so that the first call of a thread may have to make it and try again.  (By setting the device that is set: it
+// allocates nothing and waits for nothing, which would end a capture that another thread has under way.)
 template <typename F>
 cudaError_t with_context(F encode) {
     CUresult r = encode();
-    if (r != CUDA_SUCCESS && cudaFree(nullptr) == cudaSuccess) r = encode();
+    int device;
+    if (r != CUDA_SUCCESS && cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess) r = encode();
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

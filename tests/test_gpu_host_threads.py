@@ -140,3 +140,24 @@ def test_stream_zero_is_the_default_stream():
     tsl.tsenor_quantize(x, out=out, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(out.values.float(), -want.values.float()) and torch.equal(out.scales, want.scales)
+
+
+@pytest.mark.parametrize("make,size", [(_product, (64,)), (_product, (3000,)), (_step, (3, 1000, 4)), (_step, (2, 262144, 9))])
+def test_the_first_call_of_a_host_thread_while_another_captures(make, size):
+    call, args, out, _ = make(*size)
+    torch.cuda.synchronize()
+    assert call(*args) == 0
+    torch.cuda.synchronize()
+    want = out.clone()
+    out.zero_()
+    count, status, graph = torch.zeros((1,), device="cuda"), [], torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        count += 1
+        thread = threading.Thread(target=lambda: status.append(call(*args)))
+        thread.start()
+        thread.join()
+        count += 1
+    graph.replay()
+    torch.cuda.synchronize()
+    assert status == [0] and float(count) == 2 and torch.equal(out, want)
