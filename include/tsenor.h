@@ -378,7 +378,8 @@ tsenor_status tsenor_matmul(tsenor_form form, const uint8_t* a, int64_t lda, con
  * added to the counter of tsenor_error_count.  The other rows are unaffected.
  *
  * tsenor_distill_loss:  loss and lse (for tsenor_distill_grad).
- * tsenor_distill_step:  loss and gradient from one read of the logits.
+ * tsenor_distill_step:  loss and gradient in one call.  The logits are read from
+ * memory once; rows of up to 192 KB are read a second time, from L2 as a rule.
  * tsenor_distill_grad:  the gradient from lse, which the same logits gave.  A
  * rounded lse is off by 2^-24 of itself, and so is every q relative to its
  * value: rows of |lse| above 64 (low temperatures, logits far from 0) get their
@@ -387,8 +388,12 @@ tsenor_status tsenor_matmul(tsenor_form form, const uint8_t* a, int64_t lda, con
  * again.  A NaN lse fails.
  * grad has the type of the logits, ldg elements from row to row; it may be
  * the logits' own memory (same pointer, ldg == ld).  The sums are fp32 in a
- * fixed order: the same call gives the same bits.  TSENOR_ERR_SHAPE for top,
- * vocab or rows (2^24) above the limits; 1e-6 <= temperature <= 3e38.
+ * fixed order: the same call gives the same bits.  q and p are off by some
+ * 2^-20 of themselves (small ones by 2^-22 of their logarithm), the loss by that
+ * times T^2, the gradient by that times weight T (q + p): a temperature far
+ * above the spread of the logits leaves little of either.  A p below 2^-150 is
+ * 0, and its entry has no weight.  TSENOR_ERR_SHAPE for top, vocab or rows
+ * (2^24) above the limits; 1e-6 <= temperature <= 3e38.
  */
 #define TSENOR_DISTILL_MAX_TOP 1024
 #define TSENOR_DISTILL_MAX_VOCAB 262144

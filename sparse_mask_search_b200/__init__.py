@@ -592,7 +592,7 @@ def tsenor_distill_loss(logits, index, top_logits, temperature: float = 1.0, tea
 
 def tsenor_distill_step(logits, index, top_logits, temperature: float = 1.0, teacher_lse=None, weight=None, grad=None,
                         stream=None):
-    """Loss of each row and weight * d loss / d logits from one read of the logits; returns (loss, grad).
+    """Loss of each row and weight * d loss / d logits in one call; returns (loss, grad).
 
     weight: (rows,) float32, default 1: the upstream gradient of each row's loss.
     grad: optional output like the logits, which may be the logits themselves.

@@ -6,17 +6,17 @@
 //   loss = T^2 sum_j p_j (log p_j - log q_{i_j})
 //   dz_v = w T (P q_v - sum_{j: i_j = v} p_j),  P = sum_j p_j
 //
-// Bound by memory: z is read once and dz written once.  Three kernels:
+// Bound by memory: z is read from it once and dz written once.  Three kernels:
 //   stream_kernel  a row to a CTA, through registers: the loss of many rows, and the step, which reads a row again
-//                  from L2, of many rows of up to 192 KB.
-//   loss_kernel    a row cut into slices of at most 64 KB, one to a CTA of a cluster of up to 8: few rows, and the step
-//                  of longer ones.  Bulk copies bring the slice into shared memory, where its maximum, its sum of
-//                  exponentials and, for the step, its gradient are taken, and the CTAs exchange one (maximum, sum,
-//                  loss term) each.  Three CTAs to an SM overlap one row's loads with another's arithmetic and
-//                  stores.  A few rows get more and smaller slices.
-//   grad_kernel    the gradient alone, which needs nothing but z and lse.
-// Sums over the vocabulary are fp32, the few scalars of a row fp64.  Measured at 2048 x 131072 bf16, 64 entries: loss 93 us
-// (5.8 TB/s), step 227 us (4.7 TB/s), gradient 175 us (6.1 TB/s).
+//                  (from L2, as a rule), of many rows of up to 192 KB.
+//   loss_kernel    a row cut into slices, one to a CTA of a cluster of up to 8: few rows, and the step of longer ones.
+//                  Bulk copies bring the slice into shared memory, where its maximum, its sum of exponentials and, for the
+//                  step, its gradient are taken, and the CTAs exchange one (maximum, sum, loss term) each.  Slices of up to
+//                  64 KB, three CTAs to an SM, overlap one row's loads with another's arithmetic and stores; rows above
+//                  512 KB have larger ones, up to 128 KB, and two CTAs or one.  A few rows get more and smaller slices.
+//   grad_kernel    the gradient alone, which needs nothing but z and lse (rows of a large lse: a second read).
+// Sums over the vocabulary are fp32, the few scalars of a row fp64.  Measured at 2048 x 131072 bf16, 64 entries: loss 95 us
+// (5.7 TB/s), step 228 us (4.7 TB/s), gradient 160 us (6.7 TB/s; 240 us where every row has a large lse).
 #include <cfloat>
 #include <type_traits>
 
@@ -433,7 +433,7 @@ __device__ void write_loss(const DistillArgs& a, int64_t row, Norm norm, Terms s
 //   full[s]   segment s of this row is there          free[s]  its workers are done with it
 //   told[b]   the entries of a row (two buffers)      done[b]  its workers are done with them
 //   joined[j] the shares of all slices of the row
-// 2048 x 131072 bf16 227 us (4.7 TB/s), 1024 x 131072 fp32 205 us (5.2 TB/s; 227 with a CTA for each slice of each row).
+// 2048 x 131072 bf16 228 us (4.7 TB/s), 1024 x 131072 fp32 202 us (5.3 TB/s; 10 % more with a CTA for each slice of each row).
 template <typename T, bool STEP>
 __global__ void __launch_bounds__(kThreads + kTeachers, 3)
 loss_kernel(const DistillArgs a, const int slices, const int chunk_room, const int slots) {
@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const DistillArgs a, con
     teacher.template each<kThreads>(t, slice, [&](int j, int c, float) { write<T>(g + c, target[j]); });
 }
 
-// Slices of a row: at most kSliceBytes each, and for few rows enough CTAs to fill the
+// Slices of a row: at most kSliceBytes each (larger in rows that kMaxSlices of those do not hold), and for few rows enough CTAs to fill the
 // device twice, of 4 KB at least.
 int slices_of(int64_t rows, int64_t row_bytes) {
     int n = 1;

@@ -9,8 +9,8 @@
 // rounded), which more accumulators and additions outside the tensor cores would lessen at the price of a pass for each.
 // Codes stored along either axis are read as they are, K-major or MN-major.
 // Bound by the tensor cores (and, on random data, by the card's power limit) for many rows, by the bytes
-// of B for few.  Measured, with the host's share: 4096 x 28672 x 8192 nt 744 us (2.59 PFLOP/s; 486 us on zeros, where
-// the clock stays at 1965 MHz), 2048 x 11008 x 4096 82 us, 1 x 11008 x 4096 12.3 us (3.7 TB/s).
+// of B for few.  Measured, with the host's share: 4096 x 28672 x 8192 nt 757 us (2.54 PFLOP/s; 486 us on zeros, where
+// the clock stays at 1965 MHz), 2048 x 11008 x 4096 84 us, 1 x 11008 x 4096 12.3 us (3.7 TB/s).
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -43,7 +43,7 @@ __device__ unsigned long long g_stalled;
 constexpr int kTile = 128;                       // rows, columns and summed entries of a tile
 constexpr int kTileBytes = kTile * kTile;
 constexpr int kScaleBytes = 512;
-constexpr int kSms = 148;
+constexpr int kSms = 148;                        // of a B200: grids and the choice of a kernel are made for it
 constexpr int kPad = 132;                        // floats to a staged row: 16-byte stores without bank conflicts
 
 // An epilogue waits for as long as a tile's sums take: the bound grows with their number.
@@ -393,7 +393,8 @@ tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 // product may start once the 32 columns that hold the overlap have been read, which
 // the epilogue does first.  A 256 x 256 tile, because each byte that an SM takes in is used by one product only:
 // at 128 x 128 the loads alone (64 bytes a cycle and SM) took twice the products' time, here they take as long.
-// Between the two kernels the fitted costs at `launch` decide.  Five stages or four or six make no difference.
+// Between the two kernels the fitted costs at `launch` decide.  Five stages are what shared memory holds; with four
+// 2048 x 11008 x 4096 takes 76.5 us where it takes 72.0 (on one card).
 constexpr int kPairThreads = 384;                // warps: 0 loads, 1 products, 2 tensor memory, 4 to 11 epilogue
 constexpr int kPairTile = 256;
 constexpr int kPairStages = 5;
