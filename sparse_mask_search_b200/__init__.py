@@ -614,7 +614,10 @@ def tsenor_distill_step(logits, index, top_logits, temperature: float = 1.0, tea
 
 def tsenor_distill_grad(logits, index, top_logits, lse, temperature: float = 1.0, teacher_lse=None, weight=None,
                         grad=None, stream=None):
-    """weight * d loss / d logits, by the lse that tsenor_distill_loss gave for these logits; returns grad."""
+    """weight * d loss / d logits, by the lse that tsenor_distill_loss gave for these logits; returns grad.
+
+    Rows of |lse| above 64 (low temperatures, logits far from 0) are read once more: one float32 says too little there.
+    """
     import torch
     args = _distill_args(torch, logits, index, top_logits, temperature, teacher_lse)
     device = logits.device
