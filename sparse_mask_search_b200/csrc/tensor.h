@@ -136,7 +136,7 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 // Polls of a wait.  In a build for tests they are drawn: none for one wait of g_give_up_one_in, g_wait_polls for the others.
 #ifdef TSENOR_GIVE_UP
 static __device__ unsigned g_wait_polls = kTmaPolls, g_give_up_one_in;
-inline int give_up(unsigned polls, unsigned one_in) {
+static inline int give_up(unsigned polls, unsigned one_in) {
     const cudaError_t e = cudaMemcpyToSymbol(g_wait_polls, &polls, sizeof(polls));
     return e != cudaSuccess ? int(e) : int(cudaMemcpyToSymbol(g_give_up_one_in, &one_in, sizeof(one_in)));
 }
